@@ -239,8 +239,8 @@ def _run_own(s):
                                        qt=s["qt"], scale_t=s["scale_t"])
         return [v for v in got if v is not None]
     if op == "fp8":
-        return dm.dmuon_fp8_matmul(s["a"], s["a_scale"], s["b"], s["b_scale"], block_rows=s["b_rows"],
-                                   offsets=s["offsets"], out=s["c"])
+        return dm.dmuon_block_matmul(s["a"], s["a_scale"], s["b"], s["b_scale"], block_rows=s["b_rows"],
+                                     offsets=s["offsets"], out=s["c"])
     if op == "forward":
         return dm.dmuon_expert_matmul(s["x"], s["w"], s["offsets"], out=s["out"])
     if op == "input_grad":
