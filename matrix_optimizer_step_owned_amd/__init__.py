@@ -33,6 +33,8 @@ DMUON_ERR_HIP = -5
 
 DMUON_F32 = 0
 DMUON_BF16 = 1
+DMUON_E4M3 = 2
+DMUON_E5M2 = 3
 DMUON_NS_GRAM = 0
 DMUON_NS_DIRECT = 1
 DMUON_NS_PREC_BF16 = 0
@@ -86,6 +88,27 @@ class dmuon_adamw_tensor_t(ctypes.Structure):
                 ("group", ctypes.c_int32), ("pad_", ctypes.c_int32)]
 
 
+class dmuon_experts_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("ld_k", ctypes.c_int64), ("ld_n", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("experts", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class dmuon_blocks_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("block_rows", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("q_dtype", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
+class dmuon_block_product_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("experts", ctypes.c_int32), ("a_dtype", ctypes.c_int32),
+                ("b_dtype", ctypes.c_int32), ("b_block_rows", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _I64P = ctypes.POINTER(ctypes.c_int64)
@@ -127,6 +150,12 @@ EXPORTS = {
     "dmuon_assign_owners": (ctypes.c_int, [_I64P, _I64P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _HP,
                                            ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                                            ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+    "dmuon_expert_matmul": (ctypes.c_int, [ctypes.POINTER(dmuon_experts_t), _P, _P, _P, _P, _P]),
+    "dmuon_expert_input_grad": (ctypes.c_int, [ctypes.POINTER(dmuon_experts_t), _P, _P, _P, _P, _P]),
+    "dmuon_expert_weight_grad": (ctypes.c_int, [ctypes.POINTER(dmuon_experts_t), _P, _P, _P, _P, _P]),
+    "dmuon_quantize_blocks": (ctypes.c_int, [ctypes.POINTER(dmuon_blocks_t), _P, _P, _P, _P, _P, _P]),
+    "dmuon_dequantize_blocks": (ctypes.c_int, [ctypes.POINTER(dmuon_blocks_t), _P, _P, _P, _P]),
+    "dmuon_block_matmul": (ctypes.c_int, [ctypes.POINTER(dmuon_block_product_t), _P, _P, _P, _P, _P, _P, _P]),
     "dmuon_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "dmuon_last_error": (ctypes.c_char_p, []),
     "dmuon_backend_info": (ctypes.c_char_p, []),
@@ -650,6 +679,272 @@ def dmuon_clip_coefficients(grads: List[torch.Tensor], max_norm, *, norm_type: f
                                         coefs.data_ptr(), ws.data_ptr() if ws is not None else None, wsb,
                                         _stream(stream, device)), "dmuon_clip_coefficients")
     return coefs
+
+
+_Q8 = {torch.float8_e4m3fn: DMUON_E4M3, torch.float8_e5m2: DMUON_E5M2}
+_FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+class _Launch:
+    """The device a call's tensors are on, made current for the call, and the
+    stream it goes to.  Results that the call allocates belong to that
+    stream (see _workspace)."""
+
+    __slots__ = ("device", "stream", "guard")
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("tensors must be on a GPU")
+        self.device = device
+        self.stream = stream
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return _stream(self.stream, self.device)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def empty(self, shape, dtype, zero=False):
+        with torch.cuda.stream(_torch_stream(self.stream, self.device)):
+            return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self.device)
+
+
+def _rows2(t: torch.Tensor, name: str, cols: Optional[int] = None) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name} must have {cols} columns")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _rows3(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(row stride, matrix stride) of a 3-D tensor whose rows are contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return ld, (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * ld))
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _check_offsets(offsets: torch.Tensor, experts: Optional[int] = None) -> int:
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() < 2:
+        raise ValueError("offsets must be a contiguous int32 tensor of one entry per expert and one more")
+    if experts is not None and offsets.numel() != experts + 1:
+        raise ValueError(f"offsets must have {experts + 1} entries")
+    return offsets.numel() - 1
+
+
+def _expert_weights(d: dmuon_experts_t, w: torch.Tensor, name: str) -> None:
+    d.ldw, d.w_stride = _rows3(w, name)
+    d.experts, d.n, d.k = w.shape
+
+
+def dmuon_expert_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
+                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t] = w[e] @ x[t] for the rows t of expert e, offsets[e] .. offsets[e + 1] - 1
+    (x tokens x k, w experts x n x k, offsets int32 on the device).  Rows of no
+    expert are left as they were in ``out``, and are zero in an allocated result."""
+    d = dmuon_experts_t()
+    _expert_weights(d, w, "w")
+    _check_offsets(offsets, d.experts)
+    d.tokens, d.ld_k = x.shape[0], _rows2(x, "x", d.k)
+    d.dtype = _dtype(x)
+    _same_device(x.device, w=w, offsets=offsets, out=out)
+    call = _Launch(x.device, stream)
+    y = out if out is not None else call.empty((d.tokens, d.n), x.dtype, zero=True)
+    if w.dtype != x.dtype or y.dtype != x.dtype or y.shape[0] != d.tokens:
+        raise ValueError("x, w and out must share one dtype, x and out their rows")
+    d.ld_n = _rows2(y, "out", d.n)
+    with call as st:
+        _check(_lib.dmuon_expert_matmul(d, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(), st),
+               "dmuon_expert_matmul")
+    return y
+
+
+def dmuon_expert_input_grad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
+                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dx[t] = w[e].T @ dy[t]: the gradient of dmuon_expert_matmul's input."""
+    d = dmuon_experts_t()
+    _expert_weights(d, w, "w")
+    _check_offsets(offsets, d.experts)
+    d.tokens, d.ld_n = dy.shape[0], _rows2(dy, "dy", d.n)
+    d.dtype = _dtype(dy)
+    _same_device(dy.device, w=w, offsets=offsets, out=out)
+    call = _Launch(dy.device, stream)
+    dx = out if out is not None else call.empty((d.tokens, d.k), dy.dtype, zero=True)
+    if w.dtype != dy.dtype or dx.dtype != dy.dtype or dx.shape[0] != d.tokens:
+        raise ValueError("dy, w and out must share one dtype, dy and out their rows")
+    d.ld_k = _rows2(dx, "out", d.k)
+    with call as st:
+        _check(_lib.dmuon_expert_input_grad(d, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), dx.data_ptr(), st),
+               "dmuon_expert_input_grad")
+    return dx
+
+
+def dmuon_expert_weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, *,
+                             out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                             accumulate: bool = False, stream=None) -> torch.Tensor:
+    """dw[e] = dy[rows of e].T @ x[rows of e]: the gradient of dmuon_expert_matmul's
+    weights (experts x n x k, in x's dtype or float32), added to ``out`` with
+    ``accumulate``.  Each dw[e] is a gradient for dmuon_step."""
+    experts = _check_offsets(offsets)
+    d = dmuon_experts_t()
+    d.tokens, d.ld_n, d.ld_k = x.shape[0], _rows2(dy, "dy"), _rows2(x, "x")
+    d.dtype = _dtype(x)
+    _same_device(x.device, dy=dy, offsets=offsets, out=out)
+    if dy.dtype != x.dtype or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy and x must share one dtype and their rows")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    call = _Launch(x.device, stream)
+    dw = out if out is not None else call.empty((experts, dy.shape[1], x.shape[1]), out_dtype or x.dtype)
+    _expert_weights(d, dw, "out")
+    if (d.experts, d.n, d.k) != (experts, dy.shape[1], x.shape[1]):
+        raise ValueError(f"out must be {experts} x {dy.shape[1]} x {x.shape[1]}")
+    d.out_dtype, d.accumulate = _dtype(dw), 1 if accumulate else 0
+    with call as st:
+        _check(_lib.dmuon_expert_weight_grad(d, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), dw.data_ptr(), st),
+               "dmuon_expert_weight_grad")
+    return dw
+
+
+def _block_counts(rows: int, cols: int, block_rows: int) -> Tuple[int, int]:
+    return -(-rows // block_rows), -(-cols // 128)
+
+
+def _blocks_desc(x: torch.Tensor, q_dtype: torch.dtype, block_rows: int) -> dmuon_blocks_t:
+    d = dmuon_blocks_t()
+    if x.dim() == 3:
+        d.batch, d.rows, d.cols = x.shape
+        d.ldx, d.x_stride = _rows3(x, "x")
+    else:
+        d.batch, d.ldx = 1, _rows2(x, "x")
+        d.rows, d.cols = x.shape
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    d.block_rows, d.x_dtype = block_rows, _dtype(x)
+    if q_dtype not in _Q8:
+        raise TypeError(f"unsupported 8-bit dtype {q_dtype}")
+    d.q_dtype = _Q8[q_dtype]
+    return d
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def dmuon_quantize_blocks(x: torch.Tensor, *, block_rows: int = 1, fmt: str = "e4m3", transposed: bool = False,
+                          q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                          qt: Optional[torch.Tensor] = None, scale_t: Optional[torch.Tensor] = None, stream=None):
+    """(q, scale, qt, scale_t): x (rows x cols, or a batch of matrices) in
+    8-bit floating point with one fp32 scale per block_rows x 128 values, and,
+    with ``transposed`` (or given qt and scale_t), the quantised transpose; qt
+    and scale_t are None otherwise."""
+    dt = _FORMATS[fmt]
+    d = _blocks_desc(x, dt, block_rows)
+    lead = tuple(x.shape[:-2])
+    call = _Launch(x.device, stream)
+    _same_device(x.device, q=q, scale=scale, qt=qt, scale_t=scale_t)
+
+    def pair(q, s, r, c, names):
+        qs, ss = lead + (r, c), lead + _block_counts(r, c, block_rows)
+        q = _dense(q, names[0], qs, dt) if q is not None else call.empty(qs, dt)
+        s = _dense(s, names[1], ss, torch.float32) if s is not None else call.empty(ss, torch.float32)
+        return q, s
+
+    q, scale = pair(q, scale, d.rows, d.cols, ("q", "scale"))
+    if transposed or qt is not None or scale_t is not None:
+        qt, scale_t = pair(qt, scale_t, d.cols, d.rows, ("qt", "scale_t"))
+    if x.numel() == 0:
+        return q, scale, qt, scale_t
+    with call as st:
+        _check(_lib.dmuon_quantize_blocks(d, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                          qt.data_ptr() if qt is not None else None,
+                                          scale_t.data_ptr() if scale_t is not None else None, st),
+               "dmuon_quantize_blocks")
+    return q, scale, qt, scale_t
+
+
+def dmuon_dequantize_blocks(q: torch.Tensor, scale: torch.Tensor, *, block_rows: int = 1,
+                            dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """The values that (q, scale) of dmuon_quantize_blocks stand for."""
+    call = _Launch(q.device, stream)
+    _same_device(q.device, scale=scale, out=out)
+    x = out if out is not None else call.empty(q.shape, dtype)
+    if x.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    d = _blocks_desc(x, q.dtype, block_rows)
+    _dense(q, "q", q.shape, q.dtype)
+    _dense(scale, "scale", tuple(q.shape[:-2]) + _block_counts(d.rows, d.cols, block_rows), torch.float32)
+    if q.numel() == 0:
+        return x
+    with call as st:
+        _check(_lib.dmuon_dequantize_blocks(d, q.data_ptr(), scale.data_ptr(), x.data_ptr(), st),
+               "dmuon_dequantize_blocks")
+    return x
+
+
+def dmuon_block_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, *,
+                       block_rows: int = 128, offsets: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                       accumulate: bool = False, stream=None) -> torch.Tensor:
+    """c = a @ b.T of 8-bit operands with one scale per block (a m x k with
+    1 x 128 blocks, b n x k with block_rows x 128 blocks), in bfloat16 or
+    float32, added to ``out`` with ``accumulate``.  With ``offsets`` b holds
+    one matrix per expert (experts x n x k), as in dmuon_expert_matmul."""
+    d = dmuon_block_product_t()
+    m, k = a.shape[0], a.shape[-1]
+    d.m, d.k, d.lda = m, k, _rows2(a, "a")
+    lead = ()
+    if offsets is not None:
+        d.ldb, d.b_stride = _rows3(b, "b")
+        d.experts = _check_offsets(offsets, b.shape[0])
+        lead = (b.shape[0],)
+    else:
+        d.ldb = _rows2(b, "b")
+    n = b.shape[-2]
+    d.n = n
+    if b.shape[-1] != k:
+        raise ValueError("a and b must have the same number of columns")
+    if a.dtype not in _Q8 or b.dtype not in _Q8:
+        raise TypeError("a and b must be float8_e4m3fn or float8_e5m2")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    d.a_dtype, d.b_dtype, d.b_block_rows = _Q8[a.dtype], _Q8[b.dtype], block_rows
+    _same_device(a.device, a_scale=a_scale, b=b, b_scale=b_scale, offsets=offsets, out=out)
+    _dense(a_scale, "a_scale", _block_counts(m, k, 1), torch.float32)
+    _dense(b_scale, "b_scale", lead + _block_counts(n, k, block_rows), torch.float32)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    call = _Launch(a.device, stream)
+    c = out if out is not None else call.empty((m, n), out_dtype, zero=offsets is not None)
+    if c.shape[0] != m:
+        raise ValueError(f"out must have {m} rows")
+    d.ldc, d.out_dtype, d.accumulate = _rows2(c, "out", n), _dtype(c), 1 if accumulate else 0
+    with call as st:
+        _check(_lib.dmuon_block_matmul(d, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+                                       offsets.data_ptr() if offsets is not None else None, c.data_ptr(), st),
+               "dmuon_block_matmul")
+    return c
 
 
 def dmuon_plan_describe(shapes: Sequence[Sequence[int]], **hp) -> dict:

@@ -837,11 +837,10 @@ int check_device() {
 // measurement hooks
 // ---------------------------------------------------------------------------
 
-enum ProfKind { PK_MOMENTUM, PK_FINALIZE, PK_GEMM_BF16, PK_GEMM_F32, PK_UPDATE,
-                PK_CLIP_NORM, PK_CLIP_FINALIZE, PK_CLIP_SCALE, PK_GRAM_SUM, PK_ADAMW, PK_COUNT };
 const char* const kProfNames[PK_COUNT] = {"momentum", "finalize", "gemm_bf16", "gemm_f32", "update",
                                           "clip_norm", "clip_finalize", "clip_scale", "gram_sum",
-                                          "adamw"};
+                                          "adamw", "expert_bf16", "expert_f32", "quantize",
+                                          "dequantize", "block_matmul"};
 
 struct ProfRec {
   int kind;
@@ -1026,6 +1025,13 @@ std::string mat_name(const char* what, int i) { return std::string(what) + "[" +
 }  // namespace dmuon
 
 namespace dmuon {
+int check_current_device() { return check_device(); }
+
+hipError_t profiled_launch(int kind, int64_t flops, int64_t bytes, hipStream_t stream,
+                           const std::function<hipError_t()>& launch) {
+  return prof_launch(kind, flops, bytes, stream, launch);
+}
+
 int set_last_error(int status, const std::string& msg) {
   g_last_error = msg;
   return status;

@@ -1,0 +1,476 @@
+// 8-bit floating point with one fp32 scale per block of 128: quantisation,
+// its inverse, and the matrix product of quantised operands.
+//
+// Quantising a block (block_rows x 128 values; 1 x 128 for activations and
+// gradients, 128 x 128 for weights):
+//   scale = max(amax / 448 (e4m3) or 57344 (e5m2), 2^-126),  q = rne(x * (1 / scale))
+// in fp32, so amax maps to the format's largest value and nothing overflows.
+// The maximum is taken over the bit patterns of |x|, in which NaN > Inf > any
+// number: a block with a NaN or an Inf gets a non-finite scale and decodes to
+// NaN, and no other block notices.
+//
+// Product: c[i][j] = sum over blocks kb of  sa[i][kb] sb[j/bs][kb] *
+// (sum over the block's 128 k of a[i][k] b[j][k]); the scales are constant
+// within a block of k, so each block's sum is one matrix-instruction result
+// that is scaled in fp32 and added to an fp32 accumulator.
+//   - results rounded to bf16: v_mfma_f32_16x16x128_f8f6f4, one instruction
+//     per 16 x 16 x 128 block.  It aligns its products to the largest of
+//     them and keeps about 13 bits below it (measured: at most 2^-11 of the
+//     largest product per result), far below a bf16 result's own rounding.
+//   - fp32 results: the operands are widened to bf16 (exact for both
+//     formats) and go through v_mfma_f32_16x16x32_bf16, which keeps fp32
+//     sums, at half the rate.
+#include "grouped.h"
+
+namespace dmuon {
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kBlk = 128;         // values per scale along a row
+constexpr float kScaleMin = 0x1p-126f;
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t to_q8x4(float a, float b, float c, float d) {
+  int w = 0;
+  if constexpr (E5M2) {
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+  } else {
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  }
+  return uint32_t(w);
+}
+
+__device__ __forceinline__ float block_scale(uint32_t amax_bits, float max_value) {
+  const float amax = __uint_as_float(amax_bits);
+  const float s = amax / max_value;
+  return s < kScaleMin ? kScaleMin : s;   // a NaN stays
+}
+
+// ---- quantisation -----------------------------------------------------------
+
+// One 128 x 128 tile per block of 256 threads.  Thread (g, c) = (t / 16, t % 16)
+// holds columns 8c..8c+7 of rows 4g..4g+3 and 64+4g..64+4g+3: sixteen lanes
+// cover a row of 128 (its maximum is four shuffles), and four rows of a
+// column pack into one word for the transposed copy, which is turned through
+// LDS.
+template <bool F32, bool E5M2>
+__global__ void __launch_bounds__(256)
+quantize_kernel(QuantArgs P) {
+  __shared__ uint32_t row_max[kBlk], col_max[kBlk];
+  __shared__ uint32_t tr[kBlk][33];       // [column][four rows per word], one word of padding
+  const int t = threadIdx.x, g = t >> 4, c = t & 15;
+  const int rb = int((P.rows + kBlk - 1) / kBlk), cb = int((P.cols + kBlk - 1) / kBlk);
+  const int by = int(blockIdx.x) / cb, bx = int(blockIdx.x) - by * cb;
+  const int64_t batch = blockIdx.z;
+  const int64_t r0 = int64_t(by) * kBlk, c0 = int64_t(bx) * kBlk;
+  const int rows = int(P.rows - r0 < kBlk ? P.rows - r0 : kBlk);
+  const int cols = int(P.cols - c0 < kBlk ? P.cols - c0 : kBlk);
+  constexpr int EB = F32 ? 4 : 2;
+  constexpr float kMax = E5M2 ? 57344.f : 448.f;
+  const char* x = static_cast<const char*>(P.x) + (batch * P.x_stride + r0 * P.ldx + c0) * EB;
+  float v[8][8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int r = 4 * g + (q & 3) + 64 * (q >> 2);
+    const int valid = r < rows ? cols - 8 * c : 0;
+    const char* p = x + (r * P.ldx + 8 * c) * EB;
+    if constexpr (F32) {
+      u32x4_t w[2];
+      if (P.vec_x) {
+        w[0] = load_chunk<4, true>(p, valid);
+        w[1] = load_chunk<4, true>(p + 16, valid - 4);
+      } else {
+        w[0] = load_chunk<4, false>(p, valid);
+        w[1] = load_chunk<4, false>(p + 16, valid - 4);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[q][e] = __uint_as_float(w[e >> 2][e & 3]);
+    } else {
+      const u32x4_t w = P.vec_x ? load_chunk<2, true>(p, valid) : load_chunk<2, false>(p, valid);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[q][2 * e] = bf16_lo(w[e]);
+        v[q][2 * e + 1] = bf16_hi(w[e]);
+      }
+    }
+  }
+  float rinv[8];      // 1 / scale of each of the thread's rows
+  uint32_t rmax[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = __float_as_uint(v[q][e]) & 0x7fffffffu;
+      m = b > m ? b : m;
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+      const uint32_t o = __shfl_xor(m, d);
+      m = o > m ? o : m;
+    }
+    rmax[q] = m;
+  }
+  float binv = 0.f;
+  if (P.block_rows == kBlk) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) m = rmax[q] > m ? rmax[q] : m;
+    if (c == 0) row_max[g] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = row_max[i] > m ? row_max[i] : m;
+    const float s = block_scale(m, kMax);
+    binv = 1.f / s;
+    if (t == 0) {
+      if (P.scale) P.scale[(batch * rb + by) * cb + bx] = s;
+      if (P.scale_t) P.scale_t[(batch * cb + bx) * rb + by] = s;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) rinv[q] = binv;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float s = block_scale(rmax[q], kMax);
+      rinv[q] = 1.f / s;
+      const int r = 4 * g + (q & 3) + 64 * (q >> 2);
+      if (c == 0 && r < rows && P.scale) P.scale[(batch * P.rows + r0 + r) * cb + bx] = s;
+    }
+  }
+  if (P.q) {
+    uint8_t* q0 = P.q + batch * P.rows * P.cols + r0 * P.cols + c0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int r = 4 * g + (q & 3) + 64 * (q >> 2);
+      if (r >= rows || 8 * c >= cols) continue;
+      const u32x2_t w = {to_q8x4<E5M2>(v[q][0] * rinv[q], v[q][1] * rinv[q], v[q][2] * rinv[q], v[q][3] * rinv[q]),
+                         to_q8x4<E5M2>(v[q][4] * rinv[q], v[q][5] * rinv[q], v[q][6] * rinv[q], v[q][7] * rinv[q])};
+      uint8_t* p = q0 + r * P.cols + 8 * c;
+      if (P.vec_q && 8 * c + 8 <= cols) {
+        *reinterpret_cast<u32x2_t*>(p) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (8 * c + e < cols) p[e] = uint8_t(w[e >> 2] >> (8 * (e & 3)));
+      }
+    }
+  }
+  if (!P.qt) return;
+  // the transposed copy: its rows are the columns here, its blocks run along
+  // the rows here
+  float cinv[8];
+  if (P.block_rows == kBlk) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cinv[e] = binv;
+  } else {
+    if (t < kBlk) col_max[t] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t b = __float_as_uint(v[q][e]) & 0x7fffffffu;
+        m = b > m ? b : m;
+      }
+#pragma unroll
+      for (int d = 16; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_xor(m, d);
+        m = o > m ? o : m;
+      }
+      if ((t & 63) < 16) atomicMax(&col_max[8 * c + e], m);   // four waves; a maximum does not depend on the order
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cinv[e] = 1.f / block_scale(col_max[8 * c + e], kMax);
+    if (t < cols && P.scale_t)
+      P.scale_t[(batch * P.cols + c0 + t) * rb + by] = block_scale(col_max[t], kMax);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      tr[8 * c + e][g + 16 * h] = to_q8x4<E5M2>(v[4 * h][e] * cinv[e], v[4 * h + 1][e] * cinv[e],
+                                                v[4 * h + 2][e] * cinv[e], v[4 * h + 3][e] * cinv[e]);
+  __syncthreads();
+  uint8_t* qt0 = P.qt + batch * P.rows * P.cols + c0 * P.rows + r0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {     // eight lanes write one column's 128 bytes
+    const int col = (t >> 3) + 32 * i, part = (t & 7) * 16;
+    if (col >= cols || part >= rows) continue;
+    u32x4_t w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = tr[col][part / 4 + e];
+    uint8_t* p = qt0 + col * P.rows + part;
+    if (P.vec_qt && part + 16 <= rows) {
+      *reinterpret_cast<u32x4_t*>(p) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (part + e < rows) p[e] = uint8_t(w[e >> 2] >> (8 * (e & 3)));
+    }
+  }
+}
+
+template <bool E5M2>
+__device__ __forceinline__ float from_q8(uint32_t b) {
+  if constexpr (E5M2) return __builtin_amdgcn_cvt_f32_bf8(int(b), 0);
+  else return __builtin_amdgcn_cvt_f32_fp8(int(b), 0);
+}
+
+// q * scale in fp32, rounded once; one block per 128 columns x 16 rows.
+template <bool F32, bool E5M2>
+__global__ void __launch_bounds__(256)
+dequantize_kernel(QuantArgs P) {
+  const int t = threadIdx.x;
+  const int cb = int((P.cols + kBlk - 1) / kBlk);
+  const int by = int(blockIdx.x) / cb, bx = int(blockIdx.x) - by * cb;
+  const int64_t batch = blockIdx.z;
+  const int64_t r = int64_t(by) * 16 + (t >> 4), c = int64_t(bx) * kBlk + (t & 15) * 8;
+  if (r >= P.rows || c >= P.cols) return;
+  const int64_t rb = P.block_rows == kBlk ? (P.rows + kBlk - 1) / kBlk : P.rows;
+  const int64_t sr = P.block_rows == kBlk ? r / kBlk : r;
+  const float s = P.scale[(batch * rb + sr) * cb + bx];
+  const uint8_t* q = P.q + (batch * P.rows + r) * P.cols + c;
+  const int64_t at = batch * P.x_stride + r * P.ldx + c;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (c + e >= P.cols) return;
+    const float v = from_q8<E5M2>(q[e]) * s;
+    if constexpr (F32) static_cast<float*>(P.x_out)[at + e] = v;
+    else static_cast<uint16_t*>(P.x_out)[at + e] = uint16_t(pack2_bf16(v, 0.f));
+  }
+}
+
+// ---- product ----------------------------------------------------------------
+
+constexpr int kThreads = 256;
+constexpr int kOpBytes = kBlk * kBlk;     // one operand's stage: 128 rows x 128 k
+
+__device__ __forceinline__ int row_slot(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
+
+template <bool VEC>
+__device__ __forceinline__ void load_stage(const char* base, int64_t ld, int rows, int64_t k0, int64_t k,
+                                           u32x4_t (&v)[4]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = (t >> 3) + 32 * q, c = (t & 7) * 16;
+    const int64_t left = k - k0 - c;
+    v[q] = load_chunk<1, VEC>(base + r * ld + k0 + c, r < rows ? int(left > 16 ? 16 : left) : 0);
+  }
+}
+__device__ __forceinline__ void write_stage(char* lds, const u32x4_t (&v)[4]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) *reinterpret_cast<u32x4_t*>(lds + row_slot((t >> 3) + 32 * q, t & 7)) = v[q];
+}
+// A lane's 32 bytes of row r0 + lane % 16: chunks lane / 16 and lane / 16 + 4.
+// Which k a lane holds does not matter as long as both operands agree.
+__device__ __forceinline__ i32x8_t read_frag(const char* lds, int r0) {
+  const int lane = threadIdx.x & 63;
+  union { u32x4_t h[2]; i32x8_t v; } u;
+  u.h[0] = *reinterpret_cast<const u32x4_t*>(lds + row_slot(r0 + (lane & 15), lane >> 4));
+  u.h[1] = *reinterpret_cast<const u32x4_t*>(lds + row_slot(r0 + (lane & 15), 4 + (lane >> 4)));
+  return u.v;
+}
+
+template <bool E5M2>
+__device__ __forceinline__ bf16x2_t widen2(int w, bool hi) {
+  if constexpr (E5M2)
+    return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.f, true)
+              : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.f, false);
+  else
+    return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true)
+              : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false);
+}
+// Eight of a fragment's values (words 2p and 2p + 1) as bf16.
+template <bool E5M2>
+__device__ __forceinline__ bf16x8_t widen8(const i32x8_t& f, int p) {
+  union { bf16x2_t h[4]; bf16x8_t v; } u;
+  u.h[0] = widen2<E5M2>(f[2 * p], false);
+  u.h[1] = widen2<E5M2>(f[2 * p], true);
+  u.h[2] = widen2<E5M2>(f[2 * p + 1], false);
+  u.h[3] = widen2<E5M2>(f[2 * p + 1], true);
+  return u.v;
+}
+
+// Sum over one block of 128 k of a 16 x 16 piece, B first: the lane holds row
+// lane % 16 of A's rows and four consecutive ones of B's.
+template <bool A5, bool B5, bool EXACT>
+__device__ __forceinline__ f32x4_t block_product(const i32x8_t& fb, const i32x8_t& fa) {
+  f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<B5>(fb, q), widen8<A5>(fa, q), p, 0, 0, 0);
+  } else {
+    p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, p, B5 ? 1 : 0, A5 ? 1 : 0, 0, 0, 0, 0);
+  }
+  return p;
+}
+
+template <bool A5, bool B5, bool BROWS, bool VEC, typename OutT>
+__global__ void __launch_bounds__(kThreads)
+block_matmul_kernel(BlockArgs P) {
+  constexpr bool EXACT = sizeof(OutT) == 4;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * kOpBytes];
+  __shared__ float scales[2][2 * kBlk];     // A's 128 rows, B's 128 rows
+  const int64_t nt = (P.n + kBlk - 1) / kBlk;
+  int64_t mt;
+  if (P.offsets) mt = group_tiles(P.offsets, P.experts, int(P.m), kBlk);
+  else mt = (P.m + kBlk - 1) / kBlk;
+  const int64_t pos = xcd_position(blockIdx.x, mt * nt);
+  if (pos >= mt * nt) return;
+  int tm, tn, row0, end, e = 0;
+  tile_of_position(pos, mt, nt, &tm, &tn);
+  if (P.offsets) {
+    const GroupSpan g = group_of_tile(P.offsets, P.experts, int(P.m), kBlk, tm, &row0);
+    end = g.end;
+    e = g.expert;
+  } else {
+    row0 = tm * kBlk;
+    end = int(P.m);
+  }
+  const int64_t j0 = int64_t(tn) * kBlk;
+  const int rows = end - row0 < kBlk ? end - row0 : kBlk;
+  const int cols = int(P.n - j0 < kBlk ? P.n - j0 : kBlk);
+  const int64_t kb = (P.k + kBlk - 1) / kBlk;
+  const char* a = static_cast<const char*>(P.a) + row0 * P.lda;
+  const char* b = static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb;
+  // this thread's scale of a stage: threads 0-127 A's rows, 128-255 B's
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const float* sp = nullptr;
+  if (t < kBlk) {
+    if (t < rows) sp = P.a_scale + (int64_t(row0) + t) * kb;
+  } else if (t - kBlk < cols) {
+    const int64_t brows = BROWS ? P.n : nt;
+    sp = P.b_scale + (e * brows + (BROWS ? j0 + t - kBlk : tn)) * kb;
+  }
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  f32x4_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  u32x4_t va[4], vb[4];
+  float vs = 0.f;
+  load_stage<VEC>(a, P.lda, rows, 0, P.k, va);
+  load_stage<VEC>(b, P.ldb, cols, 0, P.k, vb);
+  if (sp) vs = sp[0];
+  write_stage(smem, va);
+  write_stage(smem + kOpBytes, vb);
+  scales[0][t] = vs;
+  if (kb > 1) {
+    load_stage<VEC>(a, P.lda, rows, kBlk, P.k, va);
+    load_stage<VEC>(b, P.ldb, cols, kBlk, P.k, vb);
+    if (sp) vs = sp[1];
+  }
+  for (int64_t st = 0; st < kb; ++st) {
+    char* cur = smem + (st & 1) * 2 * kOpBytes;
+    char* nxt = smem + ((st + 1) & 1) * 2 * kOpBytes;
+    const float* sc = scales[st & 1];
+    __syncthreads();
+    if (st + 1 < kb) {
+      write_stage(nxt, va);
+      write_stage(nxt + kOpBytes, vb);
+      scales[(st + 1) & 1][t] = vs;
+      if (st + 2 < kb) {
+        load_stage<VEC>(a, P.lda, rows, (st + 2) * kBlk, P.k, va);
+        load_stage<VEC>(b, P.ldb, cols, (st + 2) * kBlk, P.k, vb);
+        if (sp) vs = sp[st + 2];
+      }
+    }
+    i32x8_t fb[4];
+    f32x4_t sb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      fb[j] = read_frag(cur + kOpBytes, wn + 16 * j);
+      if constexpr (BROWS) sb[j] = *reinterpret_cast<const f32x4_t*>(sc + kBlk + wn + 16 * j + 4 * (lane >> 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const i32x8_t fa = read_frag(cur, wm + 16 * i);
+      float sa = sc[wm + 16 * i + (lane & 15)];
+      if constexpr (!BROWS) sa *= sc[kBlk];   // the tile's columns share one scale
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4_t p = block_product<A5, B5, EXACT>(fb[j], fa);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(BROWS ? sa * sb[j][r] : sa, p[r], acc[i][j][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = wm + 16 * i + (lane & 15);
+    if (r >= rows) continue;
+    OutT* row = static_cast<OutT*>(P.c) + (int64_t(row0) + r) * P.ldc + j0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), cols, P.vec_c, P.accumulate, v);
+    }
+  }
+}
+
+template <bool A5, bool B5, bool BROWS, typename OutT>
+void launch_matmul(const BlockArgs& P, bool vec, dim3 grid, hipStream_t stream) {
+  if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, OutT>), grid, dim3(kThreads), 0, stream, P);
+  else hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, false, OutT>), grid, dim3(kThreads), 0, stream, P);
+}
+template <bool A5, bool B5>
+void launch_matmul_fmt(const BlockArgs& P, bool brows, bool f32, bool vec, dim3 grid, hipStream_t stream) {
+  if (brows) {
+    if (f32) launch_matmul<A5, B5, true, float>(P, vec, grid, stream);
+    else launch_matmul<A5, B5, true, uint16_t>(P, vec, grid, stream);
+  } else {
+    if (f32) launch_matmul<A5, B5, false, float>(P, vec, grid, stream);
+    else launch_matmul<A5, B5, false, uint16_t>(P, vec, grid, stream);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_quantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((P.cols + kBlk - 1) / kBlk * ((P.rows + kBlk - 1) / kBlk)), 1,
+                  static_cast<unsigned>(P.batch));
+  const bool f32 = x_dtype == DT_F32, e5 = q_dtype == DT_E5M2;
+  if (f32 && e5) hipLaunchKernelGGL((quantize_kernel<true, true>), grid, dim3(256), 0, stream, P);
+  else if (f32) hipLaunchKernelGGL((quantize_kernel<true, false>), grid, dim3(256), 0, stream, P);
+  else if (e5) hipLaunchKernelGGL((quantize_kernel<false, true>), grid, dim3(256), 0, stream, P);
+  else hipLaunchKernelGGL((quantize_kernel<false, false>), grid, dim3(256), 0, stream, P);
+  return hipGetLastError();
+}
+
+hipError_t launch_dequantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((P.cols + kBlk - 1) / kBlk * ((P.rows + 15) / 16)), 1,
+                  static_cast<unsigned>(P.batch));
+  const bool f32 = x_dtype == DT_F32, e5 = q_dtype == DT_E5M2;
+  if (f32 && e5) hipLaunchKernelGGL((dequantize_kernel<true, true>), grid, dim3(256), 0, stream, P);
+  else if (f32) hipLaunchKernelGGL((dequantize_kernel<true, false>), grid, dim3(256), 0, stream, P);
+  else if (e5) hipLaunchKernelGGL((dequantize_kernel<false, true>), grid, dim3(256), 0, stream, P);
+  else hipLaunchKernelGGL((dequantize_kernel<false, false>), grid, dim3(256), 0, stream, P);
+  return hipGetLastError();
+}
+
+hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, bool brows, bool f32, bool vec,
+                               hipStream_t stream) {
+  const int64_t nt = (P.n + kBlk - 1) / kBlk;
+  const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
+  const dim3 grid(static_cast<unsigned>(grouped_grid((P.m / kBlk + used) * nt)));
+  if (a_dtype == DT_E5M2) {
+    if (b_dtype == DT_E5M2) launch_matmul_fmt<true, true>(P, brows, f32, vec, grid, stream);
+    else launch_matmul_fmt<true, false>(P, brows, f32, vec, grid, stream);
+  } else {
+    if (b_dtype == DT_E5M2) launch_matmul_fmt<false, true>(P, brows, f32, vec, grid, stream);
+    else launch_matmul_fmt<false, false>(P, brows, f32, vec, grid, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace dmuon

@@ -1,0 +1,346 @@
+// Matrix products of experts with ragged token counts.
+//
+// Tokens are sorted by expert: expert e has rows offsets[e] .. offsets[e+1]
+// of x (tokens x k), y and dy (tokens x n); its weights are w[e] (n x k).
+//   forward          y[t]  = w[e] x[t]                 sums over k
+//   input gradient   dx[t] = w[e]^T dy[t]              sums over n
+//   weight gradient  dw[e] = sum over its t of dy[t] x[t]^T
+// One form C[i][j] = sum_s A(i, s) B(j, s) covers the three; they differ in
+// which operand's rows run along the summed index:
+//   forward:         A = x rows      (s contiguous), B = w rows    (s contiguous)
+//   input gradient:  A = dy rows     (s contiguous), B = w columns (j contiguous)
+//   weight gradient: A = dy columns  (i contiguous), B = x columns (j contiguous)
+//
+// bf16 operands go through v_mfma_f32_16x16x32_bf16 with fp32 accumulators.
+// A contiguous-s operand sits in LDS as rows of 64 s (128 bytes) and a lane
+// reads its eight s of one row with one 16-byte read; the other kind sits as
+// 64 rows of 128 i and is read through the LDS transpose read
+// (ds_read_b64_tr_b16: sixteen lanes name a 4 x 16 piece by rows and each
+// receives one column of four), two reads for eight s.  So no operand is
+// transposed in memory.  Both LDS layouts are swizzled so that a read covers
+// all 64 banks once.  fp32 operands go through v_mfma_f32_32x32x2_f32.
+#include "grouped.h"
+
+namespace dmuon {
+namespace {
+
+constexpr int kTile = 128;        // edge of the output tile
+constexpr int kStage = 64;        // bf16: summed indices per LDS stage
+constexpr int kThreads = 256;     // four waves, 2 x 2 quadrants of 64 x 64
+
+// What one block works on: rows/cols of C that exist from the tile's corner
+// on, the length of the sum, and the corner's operand and result addresses.
+struct Work {
+  const char* a;
+  const char* b;
+  char* c;
+  int rows, cols, sum;
+  int64_t lda, ldb, ldc;   // bytes per row as stored
+};
+
+template <int OP>
+__device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int tile_n, int eb, int out_eb, Work* w) {
+  const int64_t b = blockIdx.x;
+  int tm, tn;
+  if constexpr (OP == OP_WEIGHT) {
+    const int64_t mt = (P.n + tile_m - 1) / tile_m, nt = (P.k + tile_n - 1) / tile_n;
+    const int64_t pos = xcd_position(b, mt * nt * P.experts);
+    if (pos >= mt * nt * P.experts) return false;
+    const int e = int(pos / (mt * nt));
+    tile_of_position(pos - e * mt * nt, mt, nt, &tm, &tn);
+    const GroupSpan g = group_of_expert(P.offsets, P.experts, P.tokens, e);
+    const int64_t i0 = int64_t(tm) * tile_m, j0 = int64_t(tn) * tile_n;
+    w->sum = g.end - g.begin;
+    w->rows = int(P.n - i0 < tile_m ? P.n - i0 : tile_m);
+    w->cols = int(P.k - j0 < tile_n ? P.k - j0 : tile_n);
+    w->lda = P.ld_n * eb;
+    w->ldb = P.ld_k * eb;
+    w->ldc = P.ldw * out_eb;
+    w->a = static_cast<const char*>(P.a) + g.begin * w->lda + i0 * eb;
+    w->b = static_cast<const char*>(P.b) + g.begin * w->ldb + j0 * eb;
+    w->c = static_cast<char*>(P.c) + e * P.w_stride * out_eb + i0 * w->ldc + j0 * out_eb;
+  } else {
+    const int64_t cols = OP == OP_FORWARD ? P.n : P.k;
+    const int64_t nt = (cols + tile_n - 1) / tile_n;
+    const int64_t mt = group_tiles(P.offsets, P.experts, P.tokens, tile_m);
+    const int64_t pos = xcd_position(b, mt * nt);
+    if (pos >= mt * nt) return false;
+    tile_of_position(pos, mt, nt, &tm, &tn);
+    int row0;
+    const GroupSpan g = group_of_tile(P.offsets, P.experts, P.tokens, tile_m, tm, &row0);
+    const int64_t j0 = int64_t(tn) * tile_n;
+    w->rows = g.end - row0 < tile_m ? g.end - row0 : tile_m;
+    w->cols = int(cols - j0 < tile_n ? cols - j0 : tile_n);
+    w->sum = int(OP == OP_FORWARD ? P.k : P.n);
+    w->lda = (OP == OP_FORWARD ? P.ld_k : P.ld_n) * eb;
+    w->ldb = P.ldw * eb;
+    w->ldc = (OP == OP_FORWARD ? P.ld_n : P.ld_k) * out_eb;
+    w->a = static_cast<const char*>(P.a) + row0 * w->lda;
+    w->b = static_cast<const char*>(P.b) + g.expert * P.w_stride * eb + (OP == OP_FORWARD ? j0 * w->ldb : j0 * eb);
+    w->c = static_cast<char*>(P.c) + row0 * w->ldc + j0 * out_eb;
+  }
+  return true;
+}
+
+// ---- bf16 -------------------------------------------------------------------
+
+// LDS offset of 16-byte chunk c of row r, rows of 64 s.
+__device__ __forceinline__ int row_slot(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
+// LDS offset of the 32-byte unit u (16 columns) of row s, rows of 128 columns:
+// the eight rows that half a wave's transpose read touches (s & 3 and bit 3)
+// go to eight different units.
+__device__ __forceinline__ int col_slot(int s, int u) {
+  return s * (kTile * 2) + ((u ^ ((s & 3) | ((s >> 1) & 4))) << 5);
+}
+
+// One thread's share of an operand's stage: four 16-byte chunks.
+template <bool COLS, bool VEC>
+__device__ __forceinline__ void load_stage(const char* base, int64_t ld, int extent, int s0, int sum,
+                                           u32x4_t (&v)[4]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (COLS) {   // row s, columns 8c..
+      const int s = s0 + (t >> 4) + 16 * q, c = (t & 15) * 8;
+      v[q] = load_chunk<2, VEC>(base + s * ld + c * 2, s < sum ? extent - c : 0);
+    } else {                // row r, s 8c..
+      const int r = (t >> 3) + 32 * q, c = (t & 7) * 8;
+      v[q] = load_chunk<2, VEC>(base + r * ld + (s0 + c) * 2, r < extent ? sum - s0 - c : 0);
+    }
+  }
+}
+template <bool COLS>
+__device__ __forceinline__ void write_stage(char* lds, const u32x4_t (&v)[4]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int at = COLS ? col_slot((t >> 4) + 16 * q, (t & 15) >> 1) + (t & 1) * 16
+                        : row_slot((t >> 3) + 32 * q, t & 7);
+    *reinterpret_cast<u32x4_t*>(lds + at) = v[q];
+  }
+}
+// A lane's fragment: row (or column) r0 + lane % 16, s = 32 step + 8 (lane / 16) ..
+template <bool COLS>
+__device__ __forceinline__ bf16x8_t read_frag(const char* lds, int r0, int step) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (COLS) {
+    typedef short s16x4_t __attribute__((ext_vector_type(4)));
+    const int s = 32 * step + 8 * (lane >> 4) + ((lane & 15) >> 2);
+    const char* p = lds + col_slot(s, r0 >> 4) + (lane & 3) * 8;
+    const char* q = lds + col_slot(s + 4, r0 >> 4) + (lane & 3) * 8;
+    union { s16x4_t h[2]; bf16x8_t v; } u;
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DMUON_LDS s16x4_t*)p);
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DMUON_LDS s16x4_t*)q);
+    return u.v;
+  } else {
+    return *reinterpret_cast<const bf16x8_t*>(lds + row_slot(r0 + (lane & 15), 4 * step + (lane >> 4)));
+  }
+}
+
+template <int OP, bool VEC, typename OutT>
+__global__ void __launch_bounds__(kThreads)
+expert_bf16_kernel(ExpertArgs P) {
+  constexpr bool CA = OP == OP_WEIGHT, CB = OP != OP_FORWARD;
+  constexpr int OPB = kTile * kStage * 2;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * OPB];
+  Work w;
+  if (!find_work<OP>(P, kTile, kTile, 2, sizeof(OutT), &w)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  f32x4_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int stages = (w.sum + kStage - 1) / kStage;
+  u32x4_t va[4], vb[4];
+  if (stages > 0) {
+    load_stage<CA, VEC>(w.a, w.lda, w.rows, 0, w.sum, va);
+    load_stage<CB, VEC>(w.b, w.ldb, w.cols, 0, w.sum, vb);
+    write_stage<CA>(smem, va);
+    write_stage<CB>(smem + OPB, vb);
+    if (stages > 1) {
+      load_stage<CA, VEC>(w.a, w.lda, w.rows, kStage, w.sum, va);
+      load_stage<CB, VEC>(w.b, w.ldb, w.cols, kStage, w.sum, vb);
+    }
+  }
+  for (int st = 0; st < stages; ++st) {
+    char* cur = smem + (st & 1) * 2 * OPB;
+    char* nxt = smem + ((st + 1) & 1) * 2 * OPB;
+    __syncthreads();   // stage st is written; everyone has read stage st - 1
+    if (st + 1 < stages) {
+      write_stage<CA>(nxt, va);
+      write_stage<CB>(nxt + OPB, vb);
+      if (st + 2 < stages) {
+        load_stage<CA, VEC>(w.a, w.lda, w.rows, (st + 2) * kStage, w.sum, va);
+        load_stage<CB, VEC>(w.b, w.ldb, w.cols, (st + 2) * kStage, w.sum, vb);
+      }
+    }
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      bf16x8_t fa[4], fb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[i] = read_frag<CA>(cur, wm + 16 * i, step);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fb[j] = read_frag<CB>(cur + OPB, wn + 16 * j, step);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          // B first: the lane then holds row lane % 16 and four consecutive columns
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = wm + 16 * i + (lane & 15);
+    if (r >= w.rows) continue;
+    OutT* row = reinterpret_cast<OutT*>(w.c + r * w.ldc);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), w.cols, P.vec_c, P.accumulate, v);
+    }
+  }
+}
+
+// ---- fp32 -------------------------------------------------------------------
+
+constexpr int kStageF = 16;                 // summed indices per stage
+constexpr int kPitchF = kTile + 4;          // words per LDS row (one s, 128 rows)
+
+template <bool COLS, bool VEC>
+__device__ __forceinline__ void load_stage_f(const char* base, int64_t ld, int extent, int s0, int sum,
+                                             u32x4_t (&v)[2]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if constexpr (COLS) {
+      const int s = s0 + (t >> 5) + 8 * q, c = (t & 31) * 4;
+      v[q] = load_chunk<4, VEC>(base + s * ld + c * 4, s < sum ? extent - c : 0);
+    } else {
+      const int r = (t >> 2) + 64 * q, c = (t & 3) * 4;
+      v[q] = load_chunk<4, VEC>(base + r * ld + (s0 + c) * 4, r < extent ? sum - s0 - c : 0);
+    }
+  }
+}
+template <bool COLS>
+__device__ __forceinline__ void write_stage_f(float* lds, const u32x4_t (&v)[2]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if constexpr (COLS) {
+      *reinterpret_cast<u32x4_t*>(lds + ((t >> 5) + 8 * q) * kPitchF + (t & 31) * 4) = v[q];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        lds[((t & 3) * 4 + e) * kPitchF + (t >> 2) + 64 * q] = __uint_as_float(v[q][e]);
+    }
+  }
+}
+
+template <int OP, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+expert_f32_kernel(ExpertArgs P) {
+  constexpr bool CA = OP == OP_WEIGHT, CB = OP != OP_FORWARD;
+  constexpr int OPW = kStageF * kPitchF;
+  __shared__ __attribute__((aligned(16))) float smem[4 * OPW];
+  Work w;
+  if (!find_work<OP>(P, kTile, kTile, 4, 4, &w)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const int stages = (w.sum + kStageF - 1) / kStageF;
+  u32x4_t va[2], vb[2];
+  if (stages > 0) {
+    load_stage_f<CA, VEC>(w.a, w.lda, w.rows, 0, w.sum, va);
+    load_stage_f<CB, VEC>(w.b, w.ldb, w.cols, 0, w.sum, vb);
+    write_stage_f<CA>(smem, va);
+    write_stage_f<CB>(smem + OPW, vb);
+    if (stages > 1) {
+      load_stage_f<CA, VEC>(w.a, w.lda, w.rows, kStageF, w.sum, va);
+      load_stage_f<CB, VEC>(w.b, w.ldb, w.cols, kStageF, w.sum, vb);
+    }
+  }
+  for (int st = 0; st < stages; ++st) {
+    float* cur = smem + (st & 1) * 2 * OPW;
+    float* nxt = smem + ((st + 1) & 1) * 2 * OPW;
+    __syncthreads();
+    if (st + 1 < stages) {
+      write_stage_f<CA>(nxt, va);
+      write_stage_f<CB>(nxt + OPW, vb);
+      if (st + 2 < stages) {
+        load_stage_f<CA, VEC>(w.a, w.lda, w.rows, (st + 2) * kStageF, w.sum, va);
+        load_stage_f<CB, VEC>(w.b, w.ldb, w.cols, (st + 2) * kStageF, w.sum, vb);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kStageF; s += 2) {
+      float fa[2], fb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fa[i] = cur[(s + (lane >> 5)) * kPitchF + wm + 32 * i + (lane & 31)];
+        fb[i] = cur[OPW + (s + (lane >> 5)) * kPitchF + wn + 32 * i + (lane & 31)];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = wm + 32 * i + (lane & 31);
+    if (r >= w.rows) continue;
+    float* row = reinterpret_cast<float*>(w.c + r * w.ldc);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        store4<float>(row, wn + 32 * j + 8 * g + 4 * (lane >> 5), w.cols, P.vec_c, P.accumulate, v);
+      }
+  }
+}
+
+template <int OP>
+hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hipStream_t stream) {
+  int64_t tiles;
+  if (OP == OP_WEIGHT) {
+    tiles = int64_t(P.experts) * ((P.n + kTile - 1) / kTile) * ((P.k + kTile - 1) / kTile);
+  } else {
+    const int64_t used = P.experts < P.tokens ? P.experts : P.tokens;   // experts with a partial tile
+    tiles = (P.tokens / kTile + used) * (((OP == OP_FORWARD ? P.n : P.k) + kTile - 1) / kTile);
+  }
+  const dim3 grid(static_cast<unsigned>(grouped_grid(tiles))), block(kThreads);
+  if (dtype == DT_F32) {
+    if (vec) hipLaunchKernelGGL((expert_f32_kernel<OP, true>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((expert_f32_kernel<OP, false>), grid, block, 0, stream, P);
+  } else if (OP == OP_WEIGHT && out_dtype == DT_F32) {
+    if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, float>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, float>), grid, block, 0, stream, P);
+  } else {
+    if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, uint16_t>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, uint16_t>), grid, block, 0, stream, P);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_expert_product(int op, const ExpertArgs& P, int dtype, int out_dtype, bool vec, hipStream_t stream) {
+  switch (op) {
+    case OP_FORWARD: return launch_op<OP_FORWARD>(P, dtype, out_dtype, vec, stream);
+    case OP_INPUT: return launch_op<OP_INPUT>(P, dtype, out_dtype, vec, stream);
+    default: return launch_op<OP_WEIGHT>(P, dtype, out_dtype, vec, stream);
+  }
+}
+
+}  // namespace dmuon

@@ -1,0 +1,228 @@
+// Device helpers shared by the grouped products (experts.hip, blocks.hip):
+// finding a block's expert and output tile from the device array of token
+// offsets, and 16-byte accesses of rows of any alignment.
+//
+// Offsets are device data that the host never reads, so a launch has as many
+// blocks as any offsets could need and every block works out its own tile.
+// Whatever the offsets hold, the kernels stay inside the caller's buffers:
+// every value is clamped to 0..tokens and to at least the largest value
+// before it.
+#pragma once
+
+#include "internal.h"
+
+namespace dmuon {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+#define DMUON_LDS __attribute__((address_space(3)))
+
+// One expert's rows begin..end of the token dimension.
+struct GroupSpan {
+  int expert, begin, end;
+};
+
+__device__ __forceinline__ int wave_scan_max(int v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (int(threadIdx.x & 63) >= d) v = o > v ? o : v;
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_scan_sum(int v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (int(threadIdx.x & 63) >= d) v += o;
+  }
+  return v;
+}
+
+// Sixty-four experts' spans, one per lane, and the running count of row
+// tiles: expert base + lane has rows lo..hi and row tiles before..upto.
+struct GroupChunk {
+  int lo, hi, before, upto;
+};
+__device__ __forceinline__ GroupChunk group_chunk(const int32_t* offsets, int experts, int tokens, int tile_rows,
+                                                  int base, int carry_row, int carry_tiles) {
+  const int lane = threadIdx.x & 63;
+  int v = 0;
+  if (base + lane < experts) {
+    v = offsets[base + lane + 1];
+    v = v < 0 ? 0 : v > tokens ? tokens : v;
+  }
+  if (v < carry_row) v = carry_row;
+  GroupChunk c;
+  c.hi = wave_scan_max(v);
+  const int up = __shfl_up(c.hi, 1);
+  c.lo = lane ? up : carry_row;
+  const int n = (c.hi - c.lo + tile_rows - 1) / tile_rows;
+  c.upto = carry_tiles + wave_scan_sum(n);
+  c.before = c.upto - n;
+  return c;
+}
+
+__device__ __forceinline__ int first_row(const int32_t* offsets, int tokens) {
+  const int v = offsets[0];
+  return v < 0 ? 0 : v > tokens ? tokens : v;
+}
+
+// Number of row tiles of all experts.
+__device__ __forceinline__ int group_tiles(const int32_t* offsets, int experts, int tokens, int tile_rows) {
+  int row = first_row(offsets, tokens), tiles = 0;
+  for (int base = 0; base < experts; base += 64) {
+    const GroupChunk c = group_chunk(offsets, experts, tokens, tile_rows, base, row, tiles);
+    row = __builtin_amdgcn_readlane(c.hi, 63);
+    tiles = __builtin_amdgcn_readlane(c.upto, 63);
+  }
+  return tiles;
+}
+
+// The expert of row tile `tile` (0 <= tile < group_tiles) and the tile's
+// first row; every lane of the wave gets the same answer.
+__device__ __forceinline__ GroupSpan group_of_tile(const int32_t* offsets, int experts, int tokens, int tile_rows,
+                                                   int tile, int* row0) {
+  int row = first_row(offsets, tokens), tiles = 0;
+  for (int base = 0; base < experts; base += 64) {
+    const GroupChunk c = group_chunk(offsets, experts, tokens, tile_rows, base, row, tiles);
+    const uint64_t hit = __ballot(c.upto > tile);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      GroupSpan g;
+      g.expert = base + l;
+      g.begin = __builtin_amdgcn_readlane(c.lo, l);
+      g.end = __builtin_amdgcn_readlane(c.hi, l);
+      *row0 = g.begin + (tile - __builtin_amdgcn_readlane(c.before, l)) * tile_rows;
+      return g;
+    }
+    row = __builtin_amdgcn_readlane(c.hi, 63);
+    tiles = __builtin_amdgcn_readlane(c.upto, 63);
+  }
+  *row0 = 0;
+  return GroupSpan{0, 0, 0};
+}
+
+// The rows of one expert.
+__device__ __forceinline__ GroupSpan group_of_expert(const int32_t* offsets, int experts, int tokens, int expert) {
+  int row = first_row(offsets, tokens);
+  for (int base = 0; base < experts; base += 64) {
+    const GroupChunk c = group_chunk(offsets, experts, tokens, 1, base, row, 0);
+    if (expert < base + 64) {
+      GroupSpan g;
+      g.expert = expert;
+      g.begin = __builtin_amdgcn_readlane(c.lo, expert - base);
+      g.end = __builtin_amdgcn_readlane(c.hi, expert - base);
+      return g;
+    }
+    row = __builtin_amdgcn_readlane(c.hi, 63);
+  }
+  return GroupSpan{0, 0, 0};
+}
+
+// Block -> position in the tile order.  The hardware deals blocks to the 8
+// XCDs in turn; runs of up to 32 consecutive tiles (as many blocks as an XCD
+// runs at once) go to one XCD, so that they share operand panels in its L2.
+// Positions past `total` are idle blocks; a grid of grouped_grid(bound)
+// blocks reaches every position below any total <= bound.
+__device__ __forceinline__ int64_t xcd_position(int64_t block, int64_t total) {
+  int64_t run = (total + kNumXcd - 1) / kNumXcd;
+  if (run > 32) run = 32;
+  if (run < 1) run = 1;
+  const int64_t x = block % kNumXcd, s = block / kNumXcd;
+  return ((s / run) * kNumXcd + x) * run + s % run;
+}
+inline int64_t grouped_grid(int64_t bound) { return (bound + 2 * 32 * kNumXcd - 1) / (32 * kNumXcd) * (32 * kNumXcd); }
+
+// Position -> (row tile, column tile) of a grid of tiles: eight row tiles
+// together, so the 32 blocks of an XCD cover 8 x 4 tiles.
+__device__ __forceinline__ void tile_of_position(int64_t p, int64_t mt, int64_t nt, int* tm, int* tn) {
+  const int64_t sg = p / (8 * nt);
+  const int64_t left = mt - sg * 8;
+  const int64_t gm = left < 8 ? left : 8;
+  const int64_t q = p - sg * 8 * nt;
+  *tm = int(sg * 8 + q % gm);
+  *tn = int(q / gm);
+}
+
+// Two fp32 values rounded to nearest-even bf16, packed (first in the low half).
+__device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Sixteen bytes from p, of which the first `valid` elements of EB bytes are
+// inside the row; the others read as zero.  VEC: p is 16-byte aligned and
+// `valid` is either <= 0 or a whole chunk.  Without VEC a chunk that ends
+// past the row is read element by element, nothing past the row is touched.
+template <int EB, bool VEC>
+__device__ __forceinline__ u32x4_t load_chunk(const char* p, int valid) {
+  u32x4_t v = {0, 0, 0, 0};
+  if constexpr (VEC) {
+    if (valid > 0) v = *reinterpret_cast<const u32x4_t*>(p);
+  } else {
+    struct __attribute__((packed, aligned(EB))) Any { u32x4_t v; };
+    if (valid >= 16 / EB) {
+      v = reinterpret_cast<const Any*>(p)->v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16 / EB; ++j) {
+        uint32_t e = 0;
+        if (j < valid) {
+          if constexpr (EB == 1) e = reinterpret_cast<const uint8_t*>(p)[j];
+          else if constexpr (EB == 2) e = reinterpret_cast<const uint16_t*>(p)[j];
+          else e = reinterpret_cast<const uint32_t*>(p)[j];
+        }
+        v[j * EB / 4] |= e << (8 * ((j * EB) & 3));
+      }
+    }
+  }
+  return v;
+}
+
+// Four consecutive results of a row, columns col..col+3 of n.
+template <typename OutT>
+__device__ __forceinline__ void store4(OutT* row, int col, int n, bool vec, bool accumulate, const float (&x)[4]) {
+  if (col >= n) return;
+  float v[4] = {x[0], x[1], x[2], x[3]};
+  OutT* p = row + col;
+  if (vec && col + 4 <= n) {
+    if constexpr (sizeof(OutT) == 4) {
+      if (accumulate) {
+        const f32x4_t o = *reinterpret_cast<const f32x4_t*>(p);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += o[r];
+      }
+      const f32x4_t w = {v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_t*>(p) = w;
+    } else {
+      if (accumulate) {
+        const u32x2_t o = *reinterpret_cast<const u32x2_t*>(p);
+        v[0] += bf16_lo(o[0]); v[1] += bf16_hi(o[0]); v[2] += bf16_lo(o[1]); v[3] += bf16_hi(o[1]);
+      }
+      const u32x2_t w = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+      *reinterpret_cast<u32x2_t*>(p) = w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (col + r >= n) break;
+    if constexpr (sizeof(OutT) == 4) {
+      p[r] = accumulate ? p[r] + v[r] : v[r];
+    } else {
+      if (accumulate) v[r] += bf16_lo(p[r]);
+      p[r] = static_cast<OutT>(pack2_bf16(v[r], 0.f));
+    }
+  }
+}
+
+}  // namespace dmuon

@@ -5,13 +5,14 @@
 #include <hip/hip_runtime.h>
 #include <cstddef>
 #include <cstdint>
+#include <functional>
 #include <string>
 
 #include "../../include/dmuon.h"
 
 namespace dmuon {
 
-enum : int32_t { DT_F32 = 0, DT_BF16 = 1 };
+enum : int32_t { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_E5M2 = 3 };
 
 // Edge of the square element tile of the elementwise kernels.
 constexpr int kEwTile = 64;
@@ -167,6 +168,67 @@ __device__ __forceinline__ float f64_to_f32_round_odd(double d) {
   if (fabs(back) > fabs(d)) u -= 1;   // rounded away from zero: step back toward it
   return __uint_as_float(u | 1u);
 }
+
+// ---- expert products and 8-bit blocks (experts.hip, blocks.hip) -------------
+
+// One product of experts.  a and b are x and w (forward), dy and w (input
+// gradient), dy and x (weight gradient); strides in elements.
+struct ExpertArgs {
+  const void* a;
+  const void* b;
+  void* c;
+  const int32_t* offsets;    // device, experts + 1
+  int64_t n, k;
+  int64_t ld_k, ld_n;        // rows of x / dx and of y / dy
+  int64_t ldw, w_stride;     // rows of one expert's weights, and between experts
+  int32_t experts, tokens;
+  int32_t accumulate;        // weight gradient: add to what is there
+  int32_t vec_c;             // four results of a row can be stored at once
+};
+enum { OP_FORWARD = 0, OP_INPUT = 1, OP_WEIGHT = 2 };
+// vec: every row of a and b is 16-byte aligned and a whole number of 16-byte
+// chunks along its contiguous dimension.
+hipError_t launch_expert_product(int op, const ExpertArgs& P, int dtype, int out_dtype, bool vec, hipStream_t stream);
+
+struct QuantArgs {
+  const void* x;             // quantise: source
+  void* x_out;               // dequantise: destination
+  uint8_t* q;
+  uint8_t* qt;
+  float* scale;
+  float* scale_t;
+  int64_t batch, rows, cols, ldx, x_stride;
+  int32_t block_rows;        // 1 or 128
+  int32_t vec_x, vec_q, vec_qt;   // whole-chunk accesses are aligned
+};
+hipError_t launch_quantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream);
+hipError_t launch_dequantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream);
+
+struct BlockArgs {
+  const void* a;
+  const void* b;
+  const float* a_scale;
+  const float* b_scale;
+  void* c;
+  const int32_t* offsets;    // null: one product
+  int64_t m, n, k, lda, ldb, ldc, b_stride;
+  int32_t experts;
+  int32_t accumulate;
+  int32_t vec_c;
+};
+hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, bool brows, bool f32, bool vec,
+                               hipStream_t stream);
+
+// Kernel kinds of the profiling report.
+enum ProfKind { PK_MOMENTUM, PK_FINALIZE, PK_GEMM_BF16, PK_GEMM_F32, PK_UPDATE,
+                PK_CLIP_NORM, PK_CLIP_FINALIZE, PK_CLIP_SCALE, PK_GRAM_SUM, PK_ADAMW,
+                PK_EXPERT_BF16, PK_EXPERT_F32, PK_QUANTIZE, PK_DEQUANTIZE, PK_BLOCK_MATMUL, PK_COUNT };
+
+// DMUON_OK when the current device is a gfx950, else the error's status.
+int check_current_device();
+// Runs launch(), between two events on `stream` while a profiling window is open.
+hipError_t profiled_launch(int kind, int64_t flops, int64_t bytes, hipStream_t stream,
+                           const std::function<hipError_t()>& launch);
 
 // Records msg as the calling thread's last error (dmuon_last_error) and
 // returns status; an empty message with no status clears it.
