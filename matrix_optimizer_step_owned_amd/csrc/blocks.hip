@@ -20,7 +20,7 @@
 //   - fp32 results: the operands are widened to bf16 (exact for both
 //     formats) and go through v_mfma_f32_16x16x32_bf16, which keeps fp32
 //     sums, at half the rate.
-#include "grouped.h"
+#include "bigtile.h"
 
 namespace dmuon {
 namespace {
@@ -251,8 +251,6 @@ dequantize_kernel(QuantArgs P) {
 constexpr int kThreads = 256;
 constexpr int kOpBytes = kBlk * kBlk;     // one operand's stage: 128 rows x 128 k
 
-__device__ __forceinline__ int row_slot(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
-
 template <bool VEC>
 __device__ __forceinline__ void load_stage(const char* base, int64_t ld, int rows, int64_t k0, int64_t k,
                                            u32x4_t (&v)[4]) {
@@ -320,11 +318,11 @@ block_matmul_kernel(BlockArgs P) {
   constexpr bool EXACT = sizeof(OutT) == 4;
   __shared__ __attribute__((aligned(1024))) char smem[4 * kOpBytes];
   __shared__ float scales[2][2 * kBlk];     // A's 128 rows, B's 128 rows
-  const int64_t nt = (P.n + kBlk - 1) / kBlk;
-  int64_t mt;
+  const uint32_t nt = (uint32_t(P.n) + kBlk - 1) / kBlk;
+  uint32_t mt;
   if (P.offsets) mt = group_tiles(P.offsets, P.experts, int(P.m), kBlk);
-  else mt = (P.m + kBlk - 1) / kBlk;
-  const int64_t pos = xcd_position(blockIdx.x, mt * nt);
+  else mt = (uint32_t(P.m) + kBlk - 1) / kBlk;
+  const uint32_t pos = xcd_position(blockIdx.x, mt * nt);
   if (pos >= mt * nt) return;
   int tm, tn, row0, end, e = 0;
   tile_of_position(pos, mt, nt, &tm, &tn);
@@ -348,7 +346,7 @@ block_matmul_kernel(BlockArgs P) {
   if (t < kBlk) {
     if (t < rows) sp = P.a_scale + (int64_t(row0) + t) * kb;
   } else if (t - kBlk < cols) {
-    const int64_t brows = BROWS ? P.n : nt;
+    const int64_t brows = BROWS ? P.n : int64_t(nt);
     sp = P.b_scale + (e * brows + (BROWS ? j0 + t - kBlk : tn)) * kb;
   }
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;

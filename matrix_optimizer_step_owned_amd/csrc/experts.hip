@@ -19,7 +19,9 @@
 // receives one column of four), two reads for eight s.  So no operand is
 // transposed in memory.  Both LDS layouts are swizzled so that a read covers
 // all 64 banks once.  fp32 operands go through v_mfma_f32_32x32x2_f32.
-#include "grouped.h"
+#include <type_traits>
+
+#include "bigtile.h"
 
 namespace dmuon {
 namespace {
@@ -40,13 +42,12 @@ struct Work {
 
 template <int OP>
 __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int tile_n, int eb, int out_eb, Work* w) {
-  const int64_t b = blockIdx.x;
   int tm, tn;
   if constexpr (OP == OP_WEIGHT) {
-    const int64_t mt = (P.n + tile_m - 1) / tile_m, nt = (P.k + tile_n - 1) / tile_n;
-    const int64_t pos = xcd_position(b, mt * nt * P.experts);
-    if (pos >= mt * nt * P.experts) return false;
-    const int e = int(pos / (mt * nt));
+    const uint32_t mt = (uint32_t(P.n) + tile_m - 1) / tile_m, nt = (uint32_t(P.k) + tile_n - 1) / tile_n;
+    const uint32_t total = mt * nt * P.experts, pos = xcd_position(blockIdx.x, total);
+    if (pos >= total) return false;
+    const uint32_t e = pos / (mt * nt);
     tile_of_position(pos - e * mt * nt, mt, nt, &tm, &tn);
     const GroupSpan g = group_of_expert(P.offsets, P.experts, P.tokens, e);
     const int64_t i0 = int64_t(tm) * tile_m, j0 = int64_t(tn) * tile_n;
@@ -61,9 +62,9 @@ __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int t
     w->c = static_cast<char*>(P.c) + e * P.w_stride * out_eb + i0 * w->ldc + j0 * out_eb;
   } else {
     const int64_t cols = OP == OP_FORWARD ? P.n : P.k;
-    const int64_t nt = (cols + tile_n - 1) / tile_n;
-    const int64_t mt = group_tiles(P.offsets, P.experts, P.tokens, tile_m);
-    const int64_t pos = xcd_position(b, mt * nt);
+    const uint32_t nt = (uint32_t(cols) + tile_n - 1) / tile_n;
+    const uint32_t mt = group_tiles(P.offsets, P.experts, P.tokens, tile_m);
+    const uint32_t pos = xcd_position(blockIdx.x, mt * nt);
     if (pos >= mt * nt) return false;
     tile_of_position(pos, mt, nt, &tm, &tn);
     int row0;
@@ -84,8 +85,6 @@ __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int t
 
 // ---- bf16 -------------------------------------------------------------------
 
-// LDS offset of 16-byte chunk c of row r, rows of 64 s.
-__device__ __forceinline__ int row_slot(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
 // LDS offset of the 32-byte unit u (16 columns) of row s, rows of 128 columns:
 // the eight rows that half a wave's transpose read touches (s & 3 and bit 3)
 // go to eight different units.
@@ -204,6 +203,86 @@ expert_bf16_kernel(ExpertArgs P) {
   }
 }
 
+// ---- bf16, 256 x 256 tiles ----------------------------------------------------
+
+// Tiles and stages of an expert product for the 256-tile loop (bigtile.h).
+template <int OP, typename OutT_>
+struct ExpertBig {
+  using OutT = OutT_;
+  static constexpr bool kColsA = OP == OP_WEIGHT, kColsB = OP != OP_FORWARD;
+  static constexpr bool kShort = OP != OP_WEIGHT;     // rows of weights seldom end inside a tile
+
+  const BigGroups* G;
+  uint32_t mt, nt;
+
+  // The kernel's arguments, read again at each use instead of held in scalar
+  // registers over the loop (ExpertArgs is the kernel's only parameter).
+  static __device__ __forceinline__ const ExpertArgs& args() {
+    auto* p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const ExpertArgs*)p;
+  }
+  __device__ __forceinline__ uint32_t start(BigGroups* g) {
+    const ExpertArgs& P = args();
+    G = g;
+    g->build(P.offsets, P.experts, P.tokens);
+    if constexpr (OP == OP_WEIGHT) {
+      mt = (uint32_t(P.n) + kBig - 1) / kBig;
+      nt = (uint32_t(P.k) + kBig - 1) / kBig;
+      return mt * nt * P.experts;
+    } else {
+      mt = uniform(g->tiles[P.experts]);
+      nt = (uint32_t(OP == OP_FORWARD ? P.n : P.k) + kBig - 1) / kBig;
+      return mt * nt;
+    }
+  }
+  __device__ __forceinline__ void find(uint32_t pos, BigWork* w) const {
+    const ExpertArgs& P = args();
+    int tm, tn;
+    if constexpr (OP == OP_WEIGHT) {
+      const uint32_t e = pos / (mt * nt);
+      tile_of_position(pos - e * mt * nt, mt, nt, &tm, &tn);
+      const int lo = uniform(G->rows[e]), hi = uniform(G->rows[e + 1]);
+      const int64_t i0 = int64_t(tm) * kBig, j0 = int64_t(tn) * kBig;
+      w->sum = hi - lo;
+      w->rows = int(P.n - i0 < kBig ? P.n - i0 : kBig);
+      w->cols = int(P.k - j0 < kBig ? P.k - j0 : kBig);
+      w->lda = int(P.ld_n * 2);
+      w->ldb = int(P.ld_k * 2);
+      w->ldc = int(P.ldw * int(sizeof(OutT)));
+      w->a = static_cast<const char*>(P.a) + lo * (P.ld_n * 2) + i0 * 2;
+      w->b = static_cast<const char*>(P.b) + lo * (P.ld_k * 2) + j0 * 2;
+      w->c = static_cast<char*>(P.c) + e * P.w_stride * int(sizeof(OutT)) + i0 * w->ldc + j0 * int(sizeof(OutT));
+    } else {
+      const int64_t cols = OP == OP_FORWARD ? P.n : P.k;
+      tile_of_position(pos, mt, nt, &tm, &tn);
+      const int e = G->expert_of(P.experts, tm);
+      const int row0 = uniform(G->rows[e]) + (tm - uniform(G->tiles[e])) * kBig;
+      const int end = uniform(G->rows[e + 1]);
+      const int64_t j0 = int64_t(tn) * kBig;
+      w->rows = end - row0 < kBig ? end - row0 : kBig;
+      w->cols = int(cols - j0 < kBig ? cols - j0 : kBig);
+      w->sum = int(OP == OP_FORWARD ? P.k : P.n);
+      w->lda = int((OP == OP_FORWARD ? P.ld_k : P.ld_n) * 2);
+      w->ldb = int(P.ldw * 2);
+      w->ldc = int((OP == OP_FORWARD ? P.ld_n : P.ld_k) * 2);
+      w->a = static_cast<const char*>(P.a) + int64_t(row0) * w->lda;
+      w->b = static_cast<const char*>(P.b) + e * P.w_stride * 2 + (OP == OP_FORWARD ? j0 * w->ldb : j0 * 2);
+      w->c = static_cast<char*>(P.c) + int64_t(row0) * w->ldc + j0 * 2;
+    }
+  }
+};
+
+template <int OP, typename OutT>
+__global__ void __launch_bounds__(kBigThreads)
+expert_bf16_big_kernel(ExpertArgs P) {
+  __shared__ BigSlot slot0, slot1;
+  __shared__ BigGroups groups;
+  ExpertBig<OP, OutT> op;
+  BigRun<ExpertBig<OP, OutT>> run(op, slot0.data, slot1.data, P.vec_c, P.accumulate);
+  run.run(&groups);
+}
+
 // ---- fp32 -------------------------------------------------------------------
 
 constexpr int kStageF = 16;                 // summed indices per stage
@@ -310,23 +389,41 @@ expert_f32_kernel(ExpertArgs P) {
   }
 }
 
+// Tiles of edge t that any offsets could need.
+template <int OP>
+int64_t tile_bound(const ExpertArgs& P, int64_t t) {
+  if (OP == OP_WEIGHT) return int64_t(P.experts) * ((P.n + t - 1) / t) * ((P.k + t - 1) / t);
+  const int64_t used = P.experts < P.tokens ? P.experts : P.tokens;   // experts with a partial tile
+  return (P.tokens / t + used) * (((OP == OP_FORWARD ? P.n : P.k) + t - 1) / t);
+}
+
 template <int OP>
 hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hipStream_t stream) {
-  int64_t tiles;
-  if (OP == OP_WEIGHT) {
-    tiles = int64_t(P.experts) * ((P.n + kTile - 1) / kTile) * ((P.k + kTile - 1) / kTile);
-  } else {
-    const int64_t used = P.experts < P.tokens ? P.experts : P.tokens;   // experts with a partial tile
-    tiles = (P.tokens / kTile + used) * (((OP == OP_FORWARD ? P.n : P.k) + kTile - 1) / kTile);
+  const int64_t big = tile_bound<OP>(P, kBig);
+  if (dtype == DT_BF16 && vec && big >= 128 && P.experts <= kBigExperts) {
+    const dim3 grid(static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks)), block(kBigThreads);
+    if constexpr (OP == OP_WEIGHT) {
+      if (out_dtype == DT_F32) {
+        hipLaunchKernelGGL((expert_bf16_big_kernel<OP, float>), grid, block, 0, stream, P);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((expert_bf16_big_kernel<OP, uint16_t>), grid, block, 0, stream, P);
+    return hipGetLastError();
   }
+  const int64_t tiles = tile_bound<OP>(P, kTile);
   const dim3 grid(static_cast<unsigned>(grouped_grid(tiles))), block(kThreads);
   if (dtype == DT_F32) {
     if (vec) hipLaunchKernelGGL((expert_f32_kernel<OP, true>), grid, block, 0, stream, P);
     else hipLaunchKernelGGL((expert_f32_kernel<OP, false>), grid, block, 0, stream, P);
-  } else if (OP == OP_WEIGHT && out_dtype == DT_F32) {
-    if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, float>), grid, block, 0, stream, P);
-    else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, float>), grid, block, 0, stream, P);
   } else {
+    if constexpr (OP == OP_WEIGHT) {
+      if (out_dtype == DT_F32) {
+        if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, float>), grid, block, 0, stream, P);
+        else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, float>), grid, block, 0, stream, P);
+        return hipGetLastError();
+      }
+    }
     if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, uint16_t>), grid, block, 0, stream, P);
     else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, uint16_t>), grid, block, 0, stream, P);
   }

@@ -124,29 +124,30 @@ __device__ __forceinline__ GroupSpan group_of_expert(const int32_t* offsets, int
   return GroupSpan{0, 0, 0};
 }
 
-// Block -> position in the tile order.  The hardware deals blocks to the 8
-// XCDs in turn; runs of up to 32 consecutive tiles (as many blocks as an XCD
-// runs at once) go to one XCD, so that they share operand panels in its L2.
-// Positions past `total` are idle blocks; a grid of grouped_grid(bound)
-// blocks reaches every position below any total <= bound.
-__device__ __forceinline__ int64_t xcd_position(int64_t block, int64_t total) {
-  int64_t run = (total + kNumXcd - 1) / kNumXcd;
+// Block -> position in the tile order (fewer than 2^31 tiles).  The hardware
+// deals blocks to the 8 XCDs in turn; runs of up to 32 consecutive tiles (as
+// many blocks as an XCD runs at once) go to one XCD, so that they share
+// operand panels in its L2.  Positions past `total` are idle blocks; a grid of
+// grouped_grid(bound) blocks reaches every position below any total <= bound.
+__device__ __forceinline__ uint32_t xcd_position(uint32_t block, uint32_t total) {
+  uint32_t run = (total + kNumXcd - 1) / kNumXcd;
   if (run > 32) run = 32;
   if (run < 1) run = 1;
-  const int64_t x = block % kNumXcd, s = block / kNumXcd;
+  const uint32_t x = block % kNumXcd, s = block / kNumXcd;
   return ((s / run) * kNumXcd + x) * run + s % run;
 }
 inline int64_t grouped_grid(int64_t bound) { return (bound + 2 * 32 * kNumXcd - 1) / (32 * kNumXcd) * (32 * kNumXcd); }
 
 // Position -> (row tile, column tile) of a grid of tiles: eight row tiles
 // together, so the 32 blocks of an XCD cover 8 x 4 tiles.
-__device__ __forceinline__ void tile_of_position(int64_t p, int64_t mt, int64_t nt, int* tm, int* tn) {
-  const int64_t sg = p / (8 * nt);
-  const int64_t left = mt - sg * 8;
-  const int64_t gm = left < 8 ? left : 8;
-  const int64_t q = p - sg * 8 * nt;
-  *tm = int(sg * 8 + q % gm);
-  *tn = int(q / gm);
+__device__ __forceinline__ void tile_of_position(uint32_t p, uint32_t mt, uint32_t nt, int* tm, int* tn) {
+  const uint32_t sg = p / (8 * nt);
+  const uint32_t left = mt - sg * 8;
+  const uint32_t gm = left < 8 ? left : 8;
+  const uint32_t q = p - sg * 8 * nt;
+  const uint32_t col = q / gm;
+  *tm = int(sg * 8 + (q - col * gm));
+  *tn = int(col);
 }
 
 // Two fp32 values rounded to nearest-even bf16, packed (first in the low half).
@@ -186,6 +187,22 @@ __device__ __forceinline__ u32x4_t load_chunk(const char* p, int valid) {
     }
   }
   return v;
+}
+
+// Buffer descriptor of `bytes` bytes at `base` (raw buffer, no stride), in
+// scalar registers; a lane whose offset is outside reads zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t slab_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = (uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(a >> 32))))) << 32) |
+                     uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(a))));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), static_cast<short>(0),
+                                           __builtin_amdgcn_readfirstlane(int(bytes)), 0x00020000);
+}
+constexpr uint32_t kSlabAll = 0x7ffffff0u;   // range of a descriptor whose lanes are masked by their offsets
+constexpr uint32_t kOutside = 0x80000000u;   // an offset outside every descriptor
+// Buffer load into LDS: lane l writes bytes 16l..16l+15 of the 1 KB at `lds`.
+__device__ __forceinline__ void slab_load_lds(__amdgpu_buffer_rsrc_t rsrc, char* lds, uint32_t offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (DMUON_LDS void*)lds, 16, int(offset), 0, 0, 0);
 }
 
 // Four consecutive results of a row, columns col..col+3 of n.

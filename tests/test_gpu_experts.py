@@ -53,6 +53,11 @@ CASES = [
     (640, 515, 70, offsets_of([3] * 100)),
     (1000, 384, 512, offsets_of([600, 400])),
     (64, 1000, 777, offsets_of([1] * 64)),
+    # enough 256 x 256 tiles for the kernel of that size: row tiles of 256,
+    # 200, 100 and 44 rows, a sum that ends inside a stage
+    (720, 8200, 200, offsets_of([300, 0, 100, 200, 64], 5)),
+    (720, 136, 8264, offsets_of([300, 0, 100, 200, 64], 5)),
+    (1300, 4096, 1032, offsets_of([256, 700, 12, 300])),
 ]
 
 
