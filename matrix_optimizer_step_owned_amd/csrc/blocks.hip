@@ -416,6 +416,288 @@ block_matmul_kernel(BlockArgs P) {
   }
 }
 
+// ---- product, 256 x 256 tiles --------------------------------------------------
+//
+// The tile of bigtile.h with eight waves (2 in rows x 4 in columns, 128 x 64
+// each): every block's result is scaled on the vector unit before it joins the
+// sum, so the accumulators have to be vector registers, of which a wave has
+// 256; two waves per SIMD let one wave's vector work run beside the other's
+// matrix instructions.  A stage is 128 k, one block of scales.  One barrier
+// per stage; the loads of the stage after go out right behind it.  Persistent
+// blocks, as in bigtile.h; a tile has an even number of stages.
+constexpr int kWaves8 = 8;
+constexpr int kThreads8 = kWaves8 * 64;
+constexpr int64_t kMaxBigPitch = int64_t(1) << 23;
+
+struct BlockTile {
+  const char* a;
+  const char* b;
+  const char* sa;
+  const char* sb;
+  char* c;
+  int rows, cols;      // of C from the corner on; 0 rows: no tile
+};
+
+// The stream of a wave's loads: per stage four 1 KB pieces of each operand and
+// 64 scales (waves 0-3: of A's rows, 4-7: of B's).  Past the last tile (no
+// rows) the loads read nothing.
+struct BlockStream {
+  uint32_t at_a[4], at_b[4], at_scale;
+  int first_k, lda, ldb, kb, k;
+  bool per_block;          // 128 of this wave's rows share a scale
+  const char* pa;
+  const char* pb;
+  const char* ps;
+  int rows_a, rows_b, rows_s, st;
+
+  __device__ __forceinline__ void init(int lda_, int ldb_, int k_, bool b_rows, int wave, int lane) {
+    lda = lda_;
+    ldb = ldb_;
+    k = k_;
+    kb = (k + kBlk - 1) / kBlk;
+    per_block = wave >= 4 && !b_rows;
+    first_k = ((lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7)) * 16;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t r = (wave + 8 * q) * 8 + (lane >> 3);
+      at_a[q] = r * uint32_t(lda) + first_k;
+      at_b[q] = r * uint32_t(ldb) + first_k;
+    }
+    const int r = (wave & 3) * 64 + lane;
+    at_scale = uint32_t(per_block ? r >> 7 : r) * uint32_t(kb) * 4u;
+  }
+  __device__ __forceinline__ void start(const BlockTile& t, int wave) {
+    pa = t.a;
+    pb = t.b;
+    ps = wave < 4 ? t.sa : t.sb;
+    rows_a = t.rows;
+    rows_b = t.rows > 0 ? t.cols : 0;
+    rows_s = wave < 4 ? rows_a : per_block ? (rows_b + 127) >> 7 : rows_b;
+    st = 0;
+  }
+  __device__ __forceinline__ void issue(char* slot, float* scales, int wave) {
+    const int rest = k - st * kBlk;
+    const int left = rest < 0 ? 0 : rest < kBlk ? rest : kBlk;      // of this stage's k
+    const bool none = left == 0 || rows_a == 0;
+    const uint32_t range_a = none ? 0u : uint32_t(rows_a - 1) * uint32_t(lda) + uint32_t(left);
+    const uint32_t range_b = none ? 0u : uint32_t(rows_b - 1) * uint32_t(ldb) + uint32_t(left);
+    const uint32_t range_s = none ? 0u : (uint32_t(rows_s - 1) * uint32_t(kb) + uint32_t(kb - st)) * 4u;
+    const uint32_t outside = first_k < left ? 0u : kOutside;
+    const __amdgpu_buffer_rsrc_t ra = slab_rsrc(pa, range_a), rb = slab_rsrc(pb, range_b);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) slab_load_lds(ra, slot + (wave + 8 * q) * 1024, at_a[q] | outside);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) slab_load_lds(rb, slot + kBigOp + (wave + 8 * q) * 1024, at_b[q] | outside);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(slab_rsrc(ps, range_s), (DMUON_LDS void*)(scales + wave * 64), 4,
+                                             int(at_scale), 0, 0, 0);
+    pa += kBlk;
+    pb += kBlk;
+    ps += 4;
+    ++st;
+  }
+};
+
+template <int NEWER>
+__device__ __forceinline__ void stage_barrier() {     // vmcnt(NEWER) lgkmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((NEWER & 15) | (7 << 4) | ((NEWER >> 4) << 14));
+  plain_barrier();
+}
+
+template <bool A5, bool B5, bool BROWS>
+struct BlockBig {
+  char* const slot0;
+  char* const slot1;
+  float* const sc0;
+  float* const sc1;
+  const BigGroups* const groups;
+  const int lane0, wave;
+  uint32_t mt, nt, total, pos;
+  BlockTile w, nw;
+  BlockStream loads;
+  bool stores_newer;
+  int kb;
+
+  __device__ __forceinline__ BlockBig(char* s0, char* s1, float* c0, float* c1, const BigGroups* g)
+      : slot0(s0), slot1(s1), sc0(c0), sc1(c1), groups(g), lane0(threadIdx.x & 63), wave(uniform(threadIdx.x >> 6)) {}
+
+  // The kernel's arguments, read again at each use (BlockArgs is its only parameter).
+  static __device__ __forceinline__ const BlockArgs& args() {
+    auto* p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const BlockArgs*)p;
+  }
+  __device__ __forceinline__ void find(uint32_t p, BlockTile* t) const {
+    t->rows = 0;
+    t->cols = 1;
+    if (p >= total) return;
+    const BlockArgs& P = args();
+    int tm, tn, row0, end, e = 0;
+    tile_of_position(p, mt, nt, &tm, &tn);
+    if (P.offsets) {
+      e = groups->expert_of(P.experts, tm);
+      row0 = uniform(groups->rows[e]) + (tm - uniform(groups->tiles[e])) * kBig;
+      end = uniform(groups->rows[e + 1]);
+    } else {
+      row0 = tm * kBig;
+      end = int(P.m);
+    }
+    const int64_t j0 = int64_t(tn) * kBig, n_scales = BROWS ? P.n : (P.n + kBlk - 1) / kBlk;
+    t->rows = uniform(end - row0 < kBig ? end - row0 : kBig);
+    t->cols = uniform(int(P.n - j0 < kBig ? P.n - j0 : kBig));
+    t->a = uniform_ptr(static_cast<const char*>(P.a) + row0 * P.lda);
+    t->b = uniform_ptr(static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb);
+    t->sa = uniform_ptr(reinterpret_cast<const char*>(P.a_scale + int64_t(row0) * kb));
+    t->sb = uniform_ptr(reinterpret_cast<const char*>(P.b_scale + (e * n_scales + (BROWS ? j0 : 2 * tn)) * kb));
+    t->c = uniform_ptr(static_cast<char*>(P.c) + (row0 * P.ldc + j0) * 2);
+  }
+  __device__ __forceinline__ i32x8_t frag(const char* slot, int operand, int b, int lane) const {
+    union { u32x4_t h[2]; i32x8_t v; } u;
+    u.h[0] = *reinterpret_cast<const u32x4_t*>(slot + (operand + b * 2048 + row_slot(lane & 15, lane >> 4)));
+    u.h[1] = *reinterpret_cast<const u32x4_t*>(slot + (operand + b * 2048 + row_slot(lane & 15, 4 + (lane >> 4))));
+    return u.v;
+  }
+  template <int NI>
+  __device__ __forceinline__ void multiply(const char* slot, const float* sc, f32x4_t (&acc)[NI][4]) const {
+    const int lane = here(lane0), wm = wave >> 2, wn = wave & 3;
+    i32x8_t fb[4];
+    f32x4_t sb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      fb[j] = frag(slot, kBigOp, 4 * wn + j, lane);
+      if constexpr (BROWS) sb[j] = *reinterpret_cast<const f32x4_t*>(sc + kBig + 64 * wn + 16 * j + 4 * (lane >> 4));
+    }
+    const float sb_all = BROWS ? 1.f : sc[kBig + 64 * wn];
+    // row block i's matrix instructions go out before row block i - 1's
+    // results are scaled and added; the scheduling barriers keep it at that
+    // (two row blocks of results in registers)
+    i32x8_t fa[2];
+    float sa[2];
+    f32x4_t p[2][4];
+    fa[0] = frag(slot, 0, wm, lane);
+    sa[0] = sc[16 * wm + (lane & 15)] * sb_all;
+    auto add = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = fmaf(BROWS ? sa[i & 1] * sb[j][r] : sa[i & 1], p[i & 1][j][r], acc[i][j][r]);
+      // here and not later: the compiler would keep the results for the next stage
+      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+    };
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[i & 1][j] = block_product<A5, B5, false>(fb[j], fa[i & 1]);
+      if (i > 0) add(i - 1);
+      if (i + 1 < NI) {
+        fa[(i + 1) & 1] = frag(slot, 0, 2 * (i + 1) + wm, lane);
+        sa[(i + 1) & 1] = sc[32 * (i + 1) + 16 * wm + (lane & 15)] * sb_all;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    add(NI - 1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <int NI>
+  __device__ __forceinline__ void tile() {
+    f32x4_t acc[NI][4];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int stages = (kb + 1) / 2 * 2;
+    if (stores_newer) stage_barrier<32>(); else stage_barrier<0>();
+    for (int st = 0; st < stages; st += 2) {
+      if (st) stage_barrier<0>();
+      loads.issue(slot1, sc1, wave);
+      multiply<NI>(slot0, sc0, acc);
+      stage_barrier<0>();
+      if (st + 2 >= stages) loads.start(nw, wave);
+      loads.issue(slot0, sc0, wave);
+      multiply<NI>(slot1, sc1, acc);
+    }
+    store<NI>(acc);
+  }
+  template <int NI>
+  __device__ __forceinline__ void store(const f32x4_t (&acc)[NI][4]) {
+    const BlockArgs& P = args();
+    const int lane = here(lane0);
+    const int64_t ldc = P.ldc;
+    const bool vec_c = P.vec_c, accumulate = P.accumulate;
+    const int col0 = 64 * (wave & 3) + 4 * (lane >> 4);
+    // a whole tile takes exactly 32 stores per wave, behind the loads of the
+    // next tile's first stage: its first barrier need not wait for them
+    stores_newer = NI == 8 && vec_c && !accumulate && w.rows == kBig && w.cols == kBig;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = 32 * i + 16 * (wave >> 2) + (lane & 15);
+      uint16_t* row = reinterpret_cast<uint16_t*>(w.c) + int64_t(r) * ldc;
+      if (NI == 8 && stores_newer) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const u32x2_t p = {pack2_bf16(acc[i][j][0], acc[i][j][1]), pack2_bf16(acc[i][j][2], acc[i][j][3])};
+          *reinterpret_cast<u32x2_t*>(row + col0 + 16 * j) = p;
+        }
+      } else if (r < w.rows) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+          store4<uint16_t>(row, col0 + 16 * j, w.cols, vec_c, accumulate, v);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  __device__ __forceinline__ void run(BigGroups* g) {
+    {
+      const BlockArgs& P = args();
+      kb = int((P.k + kBlk - 1) / kBlk);
+      nt = (uint32_t(P.n) + kBig - 1) / kBig;
+      if (P.offsets) {
+        g->build(P.offsets, P.experts, int(P.m));
+        mt = uniform(g->tiles[P.experts]);
+      } else {
+        mt = (uint32_t(P.m) + kBig - 1) / kBig;
+      }
+      total = mt * nt;
+      loads.init(int(P.lda), int(P.ldb), int(P.k), BROWS, wave, lane0);
+    }
+    const uint32_t grid = gridDim.x, per = grid / kNumXcd;
+    pos = grid % kNumXcd ? blockIdx.x : (blockIdx.x % kNumXcd) * per + blockIdx.x / kNumXcd;
+    find(pos, &w);
+    if (w.rows <= 0) return;
+    stores_newer = false;
+    loads.start(w, wave);
+    loads.issue(slot0, sc0, wave);
+    while (true) {
+      pos += grid;
+      find(pos, &nw);
+      if (w.rows > 128) tile<8>();
+      else if (w.rows > 64) tile<4>();
+      else tile<2>();
+      if (nw.rows <= 0) break;
+      w = nw;
+    }
+    wait_loads<0>();
+  }
+};
+
+template <bool A5, bool B5, bool BROWS>
+__global__ void __launch_bounds__(kThreads8)
+block_matmul_big_kernel(BlockArgs P) {
+  __shared__ BigSlot slot0, slot1;
+  __shared__ float sc0[2 * kBig], sc1[2 * kBig];
+  __shared__ BigGroups groups;
+  BlockBig<A5, B5, BROWS> run(slot0.data, slot1.data, sc0, sc1, &groups);
+  run.run(&groups);
+}
+
+template <bool A5, bool B5, bool BROWS>
+void launch_matmul_big(const BlockArgs& P, unsigned blocks, hipStream_t stream) {
+  hipLaunchKernelGGL((block_matmul_big_kernel<A5, B5, BROWS>), dim3(blocks), dim3(kThreads8), 0, stream, P);
+}
+
 template <bool A5, bool B5, bool BROWS, typename OutT>
 void launch_matmul(const BlockArgs& P, bool vec, dim3 grid, hipStream_t stream) {
   if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, OutT>), grid, dim3(kThreads), 0, stream, P);
@@ -458,8 +740,26 @@ hipError_t launch_dequantize(const QuantArgs& P, int x_dtype, int q_dtype, hipSt
 
 hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, bool brows, bool f32, bool vec,
                                hipStream_t stream) {
-  const int64_t nt = (P.n + kBlk - 1) / kBlk;
   const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
+  const int64_t big = (P.m / kBig + used) * ((P.n + kBig - 1) / kBig);
+  // offsets of a tile's rows within 31 bits
+  const bool fits = P.lda <= kMaxBigPitch && P.ldb <= kMaxBigPitch && P.experts <= kBigExperts;
+  if (vec && !f32 && fits && big >= 128) {
+    const unsigned blocks = static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks);
+    const int which = (a_dtype == DT_E5M2 ? 4 : 0) + (b_dtype == DT_E5M2 ? 2 : 0) + (brows ? 1 : 0);
+    switch (which) {
+      case 0: launch_matmul_big<false, false, false>(P, blocks, stream); break;
+      case 1: launch_matmul_big<false, false, true>(P, blocks, stream); break;
+      case 2: launch_matmul_big<false, true, false>(P, blocks, stream); break;
+      case 3: launch_matmul_big<false, true, true>(P, blocks, stream); break;
+      case 4: launch_matmul_big<true, false, false>(P, blocks, stream); break;
+      case 5: launch_matmul_big<true, false, true>(P, blocks, stream); break;
+      case 6: launch_matmul_big<true, true, false>(P, blocks, stream); break;
+      default: launch_matmul_big<true, true, true>(P, blocks, stream); break;
+    }
+    return hipGetLastError();
+  }
+  const int64_t nt = (P.n + kBlk - 1) / kBlk;
   const dim3 grid(static_cast<unsigned>(grouped_grid((P.m / kBlk + used) * nt)));
   if (a_dtype == DT_E5M2) {
     if (b_dtype == DT_E5M2) launch_matmul_fmt<true, true>(P, brows, f32, vec, grid, stream);

@@ -224,3 +224,44 @@ def test_replays(lib):
         for got, ref in zip((q, s, qt, st, wq, ws, y), want):
             assert torch.equal(got.view(torch.uint8) if got.element_size() == 1 else got,
                                ref.view(torch.uint8) if ref.element_size() == 1 else ref), new
+
+
+@pytest.mark.parametrize("br", [128, 1])
+@pytest.mark.parametrize("fmts", ["e4m3-e4m3", "e5m2-e4m3"])
+def test_product_large_tiles(lib, fmts, br):
+    """Enough 256 x 256 tiles for the kernel of that size: whole and short row
+    tiles, a last column tile, an odd and an even number of blocks, a sum that
+    ends inside a block; one product and experts.  A block's largest product is
+    bounded here by the product of the two rows' largest values."""
+    rng = np.random.default_rng(17)
+    fa, fb = fmts.split("-")
+
+    def large_check(got, a, sa, b, sb, old=None):
+        A, B = ob.dequantize(host(a), host(sa), 1), ob.dequantize(host(b), host(sb), br)
+        ref = A @ B.T + (0 if old is None else host(old))
+        got = got.double().cpu().numpy()
+        tol = 2.0 ** -8 * np.abs(ref) + 1e-37
+        for kb in range(0, A.shape[1], 128):
+            tol = tol + 128 * 2.0 ** -13 * np.outer(np.abs(A[:, kb:kb + 128]).max(1), np.abs(B[:, kb:kb + 128]).max(1))
+        assert np.all(np.abs(got - ref) <= tol * (1 + 1e-6))
+        assert np.linalg.norm(got - ref) <= (2.0 ** -8 + 2.0 ** -10) * np.linalg.norm(ref)
+
+    for m, n, k in ((700, 12300, 272), (300, 16400, 144), (356, 16384, 384)):
+        a, sa = quantized(rng, (m, k), 1, fa)
+        b, sb = quantized(rng, (n, k), br, fb)
+        large_check(lib.dmuon_block_matmul(a, sa, b, sb, block_rows=br), a, sa, b, sb)
+        old = make(rng, (m, n), BF)
+        acc = old.clone()
+        lib.dmuon_block_matmul(a, sa, b, sb, block_rows=br, out=acc, accumulate=True)
+        large_check(acc, a, sa, b, sb, old)
+    m, n, k, off = 600, 6200, 160, [7, 7, 300, 340, 440, 590]
+    a, sa = quantized(rng, (m, k), 1, fa)
+    b, sb = quantized(rng, (5, n, k), br, fb)
+    keep = make(rng, (m, n), BF)
+    got = keep.clone()
+    offs = torch.tensor(off, dtype=torch.int32, device=DEV)
+    lib.dmuon_block_matmul(a, sa, b, sb, block_rows=br, offsets=offs, out=got)
+    for i, lo, hi in oe.spans(off, m):
+        if hi > lo:
+            large_check(got[lo:hi], a[lo:hi], sa[lo:hi], b[i], sb[i])
+    assert torch.equal(got[:7], keep[:7]) and torch.equal(got[590:], keep[590:])
