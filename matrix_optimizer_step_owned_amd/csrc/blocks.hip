@@ -449,6 +449,8 @@ struct BlockStream {
   const char* pb;
   const char* ps;
   int rows_a, rows_b, rows_s, st;
+  __amdgpu_buffer_rsrc_t ra, rb, rs;
+  uint32_t outside;
 
   __device__ __forceinline__ void init(int lda_, int ldb_, int k_, bool b_rows, int wave, int lane) {
     lda = lda_;
@@ -475,25 +477,27 @@ struct BlockStream {
     rows_s = wave < 4 ? rows_a : per_block ? (rows_b + 127) >> 7 : rows_b;
     st = 0;
   }
-  __device__ __forceinline__ void issue(char* slot, float* scales, int wave) {
+  // Descriptors of the next stage's loads, then its nine loads one by one.
+  __device__ __forceinline__ void prepare() {
     const int rest = k - st * kBlk;
     const int left = rest < 0 ? 0 : rest < kBlk ? rest : kBlk;      // of this stage's k
     const bool none = left == 0 || rows_a == 0;
-    const uint32_t range_a = none ? 0u : uint32_t(rows_a - 1) * uint32_t(lda) + uint32_t(left);
-    const uint32_t range_b = none ? 0u : uint32_t(rows_b - 1) * uint32_t(ldb) + uint32_t(left);
-    const uint32_t range_s = none ? 0u : (uint32_t(rows_s - 1) * uint32_t(kb) + uint32_t(kb - st)) * 4u;
-    const uint32_t outside = first_k < left ? 0u : kOutside;
-    const __amdgpu_buffer_rsrc_t ra = slab_rsrc(pa, range_a), rb = slab_rsrc(pb, range_b);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) slab_load_lds(ra, slot + (wave + 8 * q) * 1024, at_a[q] | outside);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) slab_load_lds(rb, slot + kBigOp + (wave + 8 * q) * 1024, at_b[q] | outside);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(slab_rsrc(ps, range_s), (DMUON_LDS void*)(scales + wave * 64), 4,
-                                             int(at_scale), 0, 0, 0);
+    ra = slab_rsrc(pa, none ? 0u : uint32_t(rows_a - 1) * uint32_t(lda) + uint32_t(left));
+    rb = slab_rsrc(pb, none ? 0u : uint32_t(rows_b - 1) * uint32_t(ldb) + uint32_t(left));
+    rs = slab_rsrc(ps, none ? 0u : (uint32_t(rows_s - 1) * uint32_t(kb) + uint32_t(kb - st)) * 4u);
+    outside = first_k < left ? 0u : kOutside;
     pa += kBlk;
     pb += kBlk;
     ps += 4;
     ++st;
+  }
+  __device__ __forceinline__ void load(int n, char* slot, float* scales, int wave) const {
+    if (n == 8)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (DMUON_LDS void*)(scales + wave * 64), 4, int(at_scale), 0, 0, 0);
+    else if (n & 1)
+      slab_load_lds(rb, slot + kBigOp + (wave + 8 * (n >> 1)) * 1024, at_b[n >> 1] | outside);
+    else
+      slab_load_lds(ra, slot + (wave + 8 * (n >> 1)) * 1024, at_a[n >> 1] | outside);
   }
 };
 
@@ -557,9 +561,15 @@ struct BlockBig {
     u.h[1] = *reinterpret_cast<const u32x4_t*>(slot + (operand + b * 2048 + row_slot(lane & 15, 4 + (lane >> 4))));
     return u.v;
   }
+  // Loads issued before row block i of NI: all nine within the first half.
+  static constexpr int kLoadsAt(int i, int ni) { return i * 18 / ni < 9 ? i * 18 / ni : 9; }
+  // One stage from `slot`, with the loads of the next one into `to` spread over
+  // its row blocks.
   template <int NI>
-  __device__ __forceinline__ void multiply(const char* slot, const float* sc, f32x4_t (&acc)[NI][4]) const {
-    const int lane = here(lane0), wm = wave >> 2, wn = wave & 3;
+  __device__ __forceinline__ void multiply(const char* slot, const float* sc, char* to, float* to_sc,
+                                           f32x4_t (&acc)[NI][4]) {
+    const int lane = here(lane0), wm = wave >> 2, wn = wave & 3, wv = here_scalar(wave);
+    loads.prepare();
     i32x8_t fb[4];
     f32x4_t sb[4];
 #pragma unroll
@@ -594,6 +604,8 @@ struct BlockBig {
         fa[(i + 1) & 1] = frag(slot, 0, 2 * (i + 1) + wm, lane);
         sa[(i + 1) & 1] = sc[32 * (i + 1) + 16 * wm + (lane & 15)] * sb_all;
       }
+#pragma unroll
+      for (int n = kLoadsAt(i, NI); n < kLoadsAt(i + 1, NI); ++n) loads.load(n, to, to_sc, wv);
       __builtin_amdgcn_sched_barrier(0);
     }
     add(NI - 1);
@@ -610,12 +622,10 @@ struct BlockBig {
     if (stores_newer) stage_barrier<32>(); else stage_barrier<0>();
     for (int st = 0; st < stages; st += 2) {
       if (st) stage_barrier<0>();
-      loads.issue(slot1, sc1, wave);
-      multiply<NI>(slot0, sc0, acc);
+      multiply<NI>(slot0, sc0, slot1, sc1, acc);
       stage_barrier<0>();
       if (st + 2 >= stages) loads.start(nw, wave);
-      loads.issue(slot0, sc0, wave);
-      multiply<NI>(slot1, sc1, acc);
+      multiply<NI>(slot1, sc1, slot0, sc0, acc);
     }
     store<NI>(acc);
   }
@@ -669,7 +679,9 @@ struct BlockBig {
     if (w.rows <= 0) return;
     stores_newer = false;
     loads.start(w, wave);
-    loads.issue(slot0, sc0, wave);
+    loads.prepare();
+#pragma unroll
+    for (int n = 0; n < 9; ++n) loads.load(n, slot0, sc0, wave);
     while (true) {
       pos += grid;
       find(pos, &nw);
