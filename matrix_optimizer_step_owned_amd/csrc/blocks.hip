@@ -501,10 +501,9 @@ struct BlockStream {
   }
 };
 
-template <int NEWER>
-__device__ __forceinline__ void stage_barrier() {     // vmcnt(NEWER) lgkmcnt(0)
+__device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt((NEWER & 15) | (7 << 4) | ((NEWER >> 4) << 14));
+  __builtin_amdgcn_s_waitcnt(7 << 4);      // vmcnt(0) lgkmcnt(0)
   plain_barrier();
 }
 
@@ -519,7 +518,6 @@ struct BlockBig {
   uint32_t mt, nt, total, pos;
   BlockTile w, nw;
   BlockStream loads;
-  bool stores_newer;
   int kb;
 
   __device__ __forceinline__ BlockBig(char* s0, char* s1, float* c0, float* c1, const BigGroups* g)
@@ -563,52 +561,70 @@ struct BlockBig {
   }
   // Loads issued before row block i of NI: all nine within the first half.
   static constexpr int kLoadsAt(int i, int ni) { return i * 18 / ni < 9 ? i * 18 / ni : 9; }
-  // One stage from `slot`, with the loads of the next one into `to` spread over
-  // its row blocks.
-  template <int NI>
-  __device__ __forceinline__ void multiply(const char* slot, const float* sc, char* to, float* to_sc,
-                                           f32x4_t (&acc)[NI][4]) {
-    const int lane = here(lane0), wm = wave >> 2, wn = wave & 3, wv = here_scalar(wave);
-    loads.prepare();
-    i32x8_t fb[4];
+
+  // B's fragments and scales of a stage, and the first row block's of A.
+  struct Frags {
+    i32x8_t b[4], a[2];
     f32x4_t sb[4];
+    float sa[2], sb_all;
+  };
+  __device__ __forceinline__ void read_first(const char* slot, const float* sc, int lane, Frags& f) const {
+    const int wm = wave >> 2, wn = wave & 3;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      fb[j] = frag(slot, kBigOp, 4 * wn + j, lane);
-      if constexpr (BROWS) sb[j] = *reinterpret_cast<const f32x4_t*>(sc + kBig + 64 * wn + 16 * j + 4 * (lane >> 4));
+      f.b[j] = frag(slot, kBigOp, 4 * wn + j, lane);
+      if constexpr (BROWS) f.sb[j] = *reinterpret_cast<const f32x4_t*>(sc + kBig + 64 * wn + 16 * j + 4 * (lane >> 4));
     }
-    const float sb_all = BROWS ? 1.f : sc[kBig + 64 * wn];
+    f.sb_all = BROWS ? 1.f : sc[kBig + 64 * wn];
+    f.a[0] = frag(slot, 0, wm, lane);
+    f.sa[0] = sc[16 * wm + (lane & 15)] * f.sb_all;
+  }
+  // One stage from `slot`, whose first fragments are in registers, with the
+  // loads of the stage after into `to` spread over its row blocks.  Behind the
+  // last row block's matrix instructions a barrier (the next stage has landed,
+  // this one is read) and the next stage's first reads.
+  template <int NI>
+  __device__ __forceinline__ void multiply(const char* slot, const float* sc, char* to, float* to_sc, Frags& f,
+                                           f32x4_t (&acc)[NI][4]) {
+    const int lane = here(lane0), wm = wave >> 2, wv = here_scalar(wave);
+    loads.prepare();
     // row block i's matrix instructions go out before row block i - 1's
     // results are scaled and added; the scheduling barriers keep it at that
     // (two row blocks of results in registers)
-    i32x8_t fa[2];
-    float sa[2];
     f32x4_t p[2][4];
-    fa[0] = frag(slot, 0, wm, lane);
-    sa[0] = sc[16 * wm + (lane & 15)] * sb_all;
     auto add = [&](int i) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = fmaf(BROWS ? sa[i & 1] * sb[j][r] : sa[i & 1], p[i & 1][j][r], acc[i][j][r]);
+          acc[i][j][r] = fmaf(BROWS ? f.sa[i & 1] * f.sb[j][r] : f.sa[i & 1], p[i & 1][j][r], acc[i][j][r]);
       // here and not later: the compiler would keep the results for the next stage
       asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
     };
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[i & 1][j] = block_product<A5, B5, false>(fb[j], fa[i & 1]);
+      for (int j = 0; j < 4; ++j) p[i & 1][j] = block_product<A5, B5, false>(f.b[j], f.a[i & 1]);
       if (i > 0) add(i - 1);
       if (i + 1 < NI) {
-        fa[(i + 1) & 1] = frag(slot, 0, 2 * (i + 1) + wm, lane);
-        sa[(i + 1) & 1] = sc[32 * (i + 1) + 16 * wm + (lane & 15)] * sb_all;
+        f.a[(i + 1) & 1] = frag(slot, 0, 2 * (i + 1) + wm, lane);
+        f.sa[(i + 1) & 1] = sc[32 * (i + 1) + 16 * wm + (lane & 15)] * f.sb_all;
       }
 #pragma unroll
       for (int n = kLoadsAt(i, NI); n < kLoadsAt(i + 1, NI); ++n) loads.load(n, to, to_sc, wv);
       __builtin_amdgcn_sched_barrier(0);
     }
-    add(NI - 1);
+    stage_barrier();
+    if constexpr (BROWS) {
+      // the last row block still needs this stage's scales
+      add(NI - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      read_first(to, to_sc, lane, f);
+    } else {
+      static_assert(NI % 2 == 0, "the last row block's scale is in sa[1]");
+      read_first(to, to_sc, lane, f);
+      add(NI - 1);
+    }
     __builtin_amdgcn_sched_barrier(0);
   }
   template <int NI>
@@ -619,13 +635,12 @@ struct BlockBig {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     const int stages = (kb + 1) / 2 * 2;
-    if (stores_newer) stage_barrier<32>(); else stage_barrier<0>();
+    Frags f;
+    read_first(slot0, sc0, here(lane0), f);
     for (int st = 0; st < stages; st += 2) {
-      if (st) stage_barrier<0>();
-      multiply<NI>(slot0, sc0, slot1, sc1, acc);
-      stage_barrier<0>();
+      multiply<NI>(slot0, sc0, slot1, sc1, f, acc);
       if (st + 2 >= stages) loads.start(nw, wave);
-      multiply<NI>(slot1, sc1, slot0, sc0, acc);
+      multiply<NI>(slot1, sc1, slot0, sc0, f, acc);
     }
     store<NI>(acc);
   }
@@ -636,14 +651,12 @@ struct BlockBig {
     const int64_t ldc = P.ldc;
     const bool vec_c = P.vec_c, accumulate = P.accumulate;
     const int col0 = 64 * (wave & 3) + 4 * (lane >> 4);
-    // a whole tile takes exactly 32 stores per wave, behind the loads of the
-    // next tile's first stage: its first barrier need not wait for them
-    stores_newer = NI == 8 && vec_c && !accumulate && w.rows == kBig && w.cols == kBig;
+    const bool plain = vec_c && !accumulate && w.cols == kBig;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = 32 * i + 16 * (wave >> 2) + (lane & 15);
       uint16_t* row = reinterpret_cast<uint16_t*>(w.c) + int64_t(r) * ldc;
-      if (NI == 8 && stores_newer) {
+      if (r < w.rows && plain) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const u32x2_t p = {pack2_bf16(acc[i][j][0], acc[i][j][1]), pack2_bf16(acc[i][j][2], acc[i][j][3])};
@@ -677,11 +690,11 @@ struct BlockBig {
     pos = grid % kNumXcd ? blockIdx.x : (blockIdx.x % kNumXcd) * per + blockIdx.x / kNumXcd;
     find(pos, &w);
     if (w.rows <= 0) return;
-    stores_newer = false;
     loads.start(w, wave);
     loads.prepare();
 #pragma unroll
     for (int n = 0; n < 9; ++n) loads.load(n, slot0, sc0, wave);
+    stage_barrier();
     while (true) {
       pos += grid;
       find(pos, &nw);
