@@ -21,11 +21,11 @@
 //     formats) and go through v_mfma_f32_16x16x32_bf16, which keeps fp32
 //     sums, at half the rate.
 #include "bigtile.h"
+#include "skinny.h"
 
 namespace dmuon {
 namespace {
 
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kBlk = 128;         // values per scale along a row
@@ -723,8 +723,84 @@ void launch_matmul_big(const BlockArgs& P, unsigned blocks, hipStream_t stream) 
   hipLaunchKernelGGL((block_matmul_big_kernel<A5, B5, BROWS>), dim3(blocks), dim3(kThreads8), 0, stream, P);
 }
 
+// ---- product, few rows ----------------------------------------------------------
+
+template <bool A5, bool B5, bool BROWS, bool EXACT>
+struct BlockSkinny {
+  const float* sa;      // of the tile's first row; kb per row
+  const float* sb;      // of the tile's first column, or of its 128 columns
+  int64_t kb;
+
+  template <int MB>
+  __device__ __forceinline__ void step(int s, int lane, int rows, int cols, const SkinnyFrag& b,
+                                       const SkinnyFrag (&a)[MB], f32x4_t (&acc)[MB]) const {
+    const i32x8_t fb = __builtin_bit_cast(i32x8_t, b);
+    f32x4_t w;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int j = 4 * (lane >> 4) + r;
+      w[r] = sb[(BROWS ? (j < cols ? j : cols - 1) : 0) * kb + s];
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const int t = 16 * m + (lane & 15);
+      const float x = sa[(t < rows ? t : rows - 1) * kb + s];
+      const f32x4_t p = block_product<A5, B5, EXACT>(fb, __builtin_bit_cast(i32x8_t, a[m]));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(x * w[r], p[r], acc[m][r]);
+    }
+  }
+};
+
+template <bool A5, bool B5, bool BROWS, int MB, int W, typename OutT>
+__global__ void __launch_bounds__(64 * W)
+block_skinny_kernel(BlockArgs P) {
+  __shared__ __attribute__((aligned(16))) float sums[W * MB * 256];
+  const uint32_t nt = (uint32_t(P.n) + 15) / 16;
+  const uint32_t tm = blockIdx.x / nt, tn = blockIdx.x - tm * nt;
+  int row0 = int(tm) * 16 * MB, end = int(P.m), e = 0;
+  if (P.offsets) {
+    const GroupSpan g = group_of_tile(P.offsets, P.experts, int(P.m), 16 * MB, tm, &row0);
+    end = g.end;
+    e = g.expert;
+  }
+  if (row0 >= end) return;
+  const int64_t j0 = int64_t(tn) * 16, kb = (P.k + kBlk - 1) / kBlk;
+  const int64_t b_scales = BROWS ? P.n : (P.n + kBlk - 1) / kBlk;
+  BlockSkinny<A5, B5, BROWS, sizeof(OutT) == 4> op;
+  op.sa = P.a_scale + int64_t(row0) * kb;
+  op.sb = P.b_scale + (e * b_scales + (BROWS ? j0 : j0 / kBlk)) * kb;
+  op.kb = kb;
+  skinny_block<decltype(op), MB, W, OutT>(op, static_cast<const char*>(P.a) + row0 * P.lda, P.lda,
+                                          static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb, P.ldb,
+                                          static_cast<OutT*>(P.c) + row0 * P.ldc + j0, P.ldc,
+                                          end - row0 < 16 * MB ? end - row0 : 16 * MB,
+                                          int(P.n - j0 < 16 ? P.n - j0 : 16), P.k, P.vec_c, P.accumulate, sums);
+}
+
+int64_t skinny_blocks(const BlockArgs& P, int mb) {
+  const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
+  return (P.m / (16 * mb) + used) * ((P.n + 15) / 16);
+}
+template <bool A5, bool B5, bool BROWS, int MB, typename OutT>
+void launch_skinny(const BlockArgs& P, hipStream_t stream) {
+  const int64_t blocks = skinny_blocks(P, MB);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  switch (skinny_waves(blocks)) {
+    case 4: hipLaunchKernelGGL((block_skinny_kernel<A5, B5, BROWS, MB, 4, OutT>), grid, dim3(256), 0, stream, P); break;
+    case 8: hipLaunchKernelGGL((block_skinny_kernel<A5, B5, BROWS, MB, 8, OutT>), grid, dim3(512), 0, stream, P); break;
+    default: hipLaunchKernelGGL((block_skinny_kernel<A5, B5, BROWS, MB, 16, OutT>), grid, dim3(1024), 0, stream, P); break;
+  }
+}
+
 template <bool A5, bool B5, bool BROWS, typename OutT>
 void launch_matmul(const BlockArgs& P, bool vec, dim3 grid, hipStream_t stream) {
+  // at most 16, or 32, rows per expert on average
+  const int64_t experts = P.offsets ? P.experts : 1;
+  if (vec && skinny_blocks(P, 1) <= kMaxSkinnyBlocks) {
+    if (P.m <= 16 * experts) return launch_skinny<A5, B5, BROWS, 1, OutT>(P, stream);
+    if (P.m <= 32 * experts) return launch_skinny<A5, B5, BROWS, 2, OutT>(P, stream);
+  }
   if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, OutT>), grid, dim3(kThreads), 0, stream, P);
   else hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, false, OutT>), grid, dim3(kThreads), 0, stream, P);
 }
@@ -769,7 +845,8 @@ hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, boo
   const int64_t big = (P.m / kBig + used) * ((P.n + kBig - 1) / kBig);
   // offsets of a tile's rows within 31 bits
   const bool fits = P.lda <= kMaxBigPitch && P.ldb <= kMaxBigPitch && P.experts <= kBigExperts;
-  if (vec && !f32 && fits && big >= 128) {
+  const bool few = P.m <= 32 * int64_t(P.offsets ? P.experts : 1);
+  if (vec && !f32 && fits && big >= 128 && !few) {
     const unsigned blocks = static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks);
     const int which = (a_dtype == DT_E5M2 ? 4 : 0) + (b_dtype == DT_E5M2 ? 2 : 0) + (brows ? 1 : 0);
     switch (which) {

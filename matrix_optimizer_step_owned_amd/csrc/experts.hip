@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "bigtile.h"
+#include "skinny.h"
 
 namespace dmuon {
 namespace {
@@ -283,6 +284,55 @@ expert_bf16_big_kernel(ExpertArgs P) {
   run.run(&groups);
 }
 
+// ---- bf16, few rows per expert (forward) ---------------------------------------
+
+struct ExpertSkinny {
+  template <int MB>
+  __device__ __forceinline__ void step(int, int, int, int, const SkinnyFrag& b, const SkinnyFrag (&a)[MB],
+                                       f32x4_t (&acc)[MB]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b.h[h]),
+                                                         __builtin_bit_cast(bf16x8_t, a[m].h[h]), acc[m], 0, 0, 0);
+  }
+};
+
+// Row tiles of 16 MB rows by column tiles of 16.
+template <int MB, int W>
+__global__ void __launch_bounds__(64 * W)
+expert_skinny_kernel(ExpertArgs P) {
+  __shared__ __attribute__((aligned(16))) float sums[W * MB * 256];
+  const uint32_t nt = (uint32_t(P.n) + 15) / 16;
+  const uint32_t tm = blockIdx.x / nt, tn = blockIdx.x - tm * nt;
+  int row0;
+  const GroupSpan g = group_of_tile(P.offsets, P.experts, P.tokens, 16 * MB, tm, &row0);
+  if (row0 >= g.end) return;                // past the last tile
+  const int64_t j0 = int64_t(tn) * 16;
+  skinny_block<ExpertSkinny, MB, W, uint16_t>(
+      ExpertSkinny{}, static_cast<const char*>(P.a) + row0 * P.ld_k * 2, P.ld_k * 2,
+      static_cast<const char*>(P.b) + (g.expert * P.w_stride + j0 * P.ldw) * 2, P.ldw * 2,
+      static_cast<uint16_t*>(P.c) + row0 * P.ld_n + j0, P.ld_n, g.end - row0 < 16 * MB ? g.end - row0 : 16 * MB,
+      int(P.n - j0 < 16 ? P.n - j0 : 16), P.k * 2, P.vec_c, false, sums);
+}
+
+int64_t skinny_blocks(const ExpertArgs& P, int mb) {
+  const int64_t used = P.experts < P.tokens ? P.experts : P.tokens;
+  return (P.tokens / (16 * mb) + used) * ((P.n + 15) / 16);
+}
+template <int MB>
+hipError_t launch_skinny(const ExpertArgs& P, hipStream_t stream) {
+  const int64_t blocks = skinny_blocks(P, MB);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  switch (skinny_waves(blocks)) {
+    case 4: hipLaunchKernelGGL((expert_skinny_kernel<MB, 4>), grid, dim3(256), 0, stream, P); break;
+    case 8: hipLaunchKernelGGL((expert_skinny_kernel<MB, 8>), grid, dim3(512), 0, stream, P); break;
+    default: hipLaunchKernelGGL((expert_skinny_kernel<MB, 16>), grid, dim3(1024), 0, stream, P); break;
+  }
+  return hipGetLastError();
+}
+
 // ---- fp32 -------------------------------------------------------------------
 
 constexpr int kStageF = 16;                 // summed indices per stage
@@ -399,6 +449,13 @@ int64_t tile_bound(const ExpertArgs& P, int64_t t) {
 
 template <int OP>
 hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hipStream_t stream) {
+  if constexpr (OP == OP_FORWARD) {
+    // at most 16, or 32, rows per expert on average
+    if (dtype == DT_BF16 && vec && skinny_blocks(P, 1) <= kMaxSkinnyBlocks) {
+      if (P.tokens <= 16 * int64_t(P.experts)) return launch_skinny<1>(P, stream);
+      if (P.tokens <= 32 * int64_t(P.experts)) return launch_skinny<2>(P, stream);
+    }
+  }
   const int64_t big = tile_bound<OP>(P, kBig);
   if (dtype == DT_BF16 && vec && big >= 128 && P.experts <= kBigExperts) {
     const dim3 grid(static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks)), block(kBigThreads);

@@ -132,7 +132,7 @@ def check(got, a, sa, b, sb, br, old=None):
 
 
 PRODUCTS = [(1, 1, 1), (2, 40, 130), (7, 256, 512), (16, 100, 16), (33, 129, 257), (128, 128, 128), (130, 260, 384),
-            (200, 72, 1000), (300, 300, 48)]
+            (200, 72, 1000), (300, 300, 48), (5, 4200, 144), (20, 8200, 272), (16, 36, 2064)]
 
 
 @pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])

@@ -53,6 +53,11 @@ CASES = [
     (640, 515, 70, offsets_of([3] * 100)),
     (1000, 384, 512, offsets_of([600, 400])),
     (64, 1000, 777, offsets_of([1] * 64)),
+    # few rows per expert: one and two blocks of 16 rows, 16, 8 and 4 waves
+    (33, 260, 520, offsets_of([1, 0, 3, 16, 2, 11])),
+    (100, 72, 1032, offsets_of([40, 1, 30, 29])),
+    (9, 2100, 136, offsets_of([2, 6], 1)),
+    (45, 8200, 72, offsets_of([2, 43])),
     # enough 256 x 256 tiles for the kernel of that size: row tiles of 256,
     # 200, 100 and 44 rows, a sum that ends inside a stage
     (720, 8200, 200, offsets_of([300, 0, 100, 200, 64], 5)),
