@@ -685,74 +685,96 @@ _Q8 = {torch.float8_e4m3fn: DMUON_E4M3, torch.float8_e5m2: DMUON_E5M2}
 _FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 
 
-class _Launch:
-    """The device a call's tensors are on, made current for the call, and the
-    stream it goes to.  Results that the call allocates belong to that
-    stream (see _workspace)."""
-
-    __slots__ = ("device", "stream", "guard")
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("tensors must be on a GPU")
-        self.device = device
-        self.stream = stream
-        self.guard = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return _stream(self.stream, self.device)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-    def empty(self, shape, dtype, zero=False):
-        with torch.cuda.stream(_torch_stream(self.stream, self.device)):
-            return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self.device)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows2(t: torch.Tensor, name: str, cols: Optional[int] = None) -> int:
-    """Row stride of a 2-D tensor whose rows are contiguous."""
+def _launch(f, name: str, device, stream, *args) -> None:
+    """Calls a C entry point on the device of its tensors and on the current
+    (or the given) stream."""
+    index = device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            status = f(*args, _raw_stream(index) if stream is None else _stream(stream, device))
+    else:
+        status = f(*args, _raw_stream(index) if stream is None else _stream(stream, device))
+    if status != DMUON_OK:
+        raise DmuonError(status, name)
+
+
+def _gpu(t: torch.Tensor):
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    return t.device
+
+
+def _result(device, stream, shape, dtype, zero=False) -> torch.Tensor:
+    """A result allocated here: it belongs to the stream the call runs on (see
+    _workspace)."""
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+
+
+def _rows2(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, columns, row stride) of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError(f"{name} must have {cols} columns")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    return rows, cols, ld if rows > 1 else cols if ld < cols else ld
 
 
-def _rows3(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(row stride, matrix stride) of a 3-D tensor whose rows are contiguous."""
+def _rows3(t: torch.Tensor, name: str) -> Tuple[int, int, int, int, int]:
+    """(matrices, rows, columns, row stride, matrix stride) of a 3-D tensor
+    whose rows are contiguous."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    n, rows, cols = t.shape
+    far, ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return ld, (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * ld))
+    if rows <= 1:
+        ld = cols
+    return n, rows, cols, ld, far if n > 1 else rows * ld
 
 
-def _same_device(device, **tensors) -> None:
-    for name, t in tensors.items():
+def _same_device(device, *tensors) -> None:
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not {device}")
+            raise ValueError(f"a tensor is on {t.device}, not {device}")
 
 
-def _check_offsets(offsets: torch.Tensor, experts: Optional[int] = None) -> int:
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() < 2:
+def _check_offsets(offsets: torch.Tensor) -> int:
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 tensor of one entry per expert and one more")
-    if experts is not None and offsets.numel() != experts + 1:
+    return offsets.shape[0] - 1
+
+
+def _expert_rows(f, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                 out: Optional[torch.Tensor], stream, forward: bool) -> torch.Tensor:
+    """dmuon_expert_matmul and dmuon_expert_input_grad: rows in, rows out."""
+    experts, n, k, ldw, far = _rows3(w, "w")
+    tokens, cols, lda = _rows2(a, "x" if forward else "dy")
+    if cols != (k if forward else n):
+        raise ValueError(f"{'x' if forward else 'dy'} must have {k if forward else n} columns")
+    if _check_offsets(offsets) != experts:
         raise ValueError(f"offsets must have {experts + 1} entries")
-    return offsets.numel() - 1
-
-
-def _expert_weights(d: dmuon_experts_t, w: torch.Tensor, name: str) -> None:
-    d.ldw, d.w_stride = _rows3(w, name)
-    d.experts, d.n, d.k = w.shape
+    dt = a.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    device = _gpu(a)
+    width = n if forward else k
+    if out is None:
+        out = _result(device, stream, (tokens, width), dt, zero=True)
+    rows, cols, ldo = _rows2(out, "out")
+    if w.dtype != dt or out.dtype != dt or rows != tokens or cols != width:
+        raise ValueError(f"w and out must be {dt}, out {tokens} x {width}")
+    _same_device(device, w, offsets, out)
+    d = dmuon_experts_t(tokens, n, k, lda if forward else ldo, ldo if forward else lda, ldw, far, experts,
+                        _DTYPES[dt])
+    _launch(f, name, device, stream, d, a.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    return out
 
 
 def dmuon_expert_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
@@ -760,41 +782,13 @@ def dmuon_expert_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     """y[t] = w[e] @ x[t] for the rows t of expert e, offsets[e] .. offsets[e + 1] - 1
     (x tokens x k, w experts x n x k, offsets int32 on the device).  Rows of no
     expert are left as they were in ``out``, and are zero in an allocated result."""
-    d = dmuon_experts_t()
-    _expert_weights(d, w, "w")
-    _check_offsets(offsets, d.experts)
-    d.tokens, d.ld_k = x.shape[0], _rows2(x, "x", d.k)
-    d.dtype = _dtype(x)
-    _same_device(x.device, w=w, offsets=offsets, out=out)
-    call = _Launch(x.device, stream)
-    y = out if out is not None else call.empty((d.tokens, d.n), x.dtype, zero=True)
-    if w.dtype != x.dtype or y.dtype != x.dtype or y.shape[0] != d.tokens:
-        raise ValueError("x, w and out must share one dtype, x and out their rows")
-    d.ld_n = _rows2(y, "out", d.n)
-    with call as st:
-        _check(_lib.dmuon_expert_matmul(d, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(), st),
-               "dmuon_expert_matmul")
-    return y
+    return _expert_rows(_lib.dmuon_expert_matmul, "dmuon_expert_matmul", x, w, offsets, out, stream, True)
 
 
 def dmuon_expert_input_grad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dx[t] = w[e].T @ dy[t]: the gradient of dmuon_expert_matmul's input."""
-    d = dmuon_experts_t()
-    _expert_weights(d, w, "w")
-    _check_offsets(offsets, d.experts)
-    d.tokens, d.ld_n = dy.shape[0], _rows2(dy, "dy", d.n)
-    d.dtype = _dtype(dy)
-    _same_device(dy.device, w=w, offsets=offsets, out=out)
-    call = _Launch(dy.device, stream)
-    dx = out if out is not None else call.empty((d.tokens, d.k), dy.dtype, zero=True)
-    if w.dtype != dy.dtype or dx.dtype != dy.dtype or dx.shape[0] != d.tokens:
-        raise ValueError("dy, w and out must share one dtype, dy and out their rows")
-    d.ld_k = _rows2(dx, "out", d.k)
-    with call as st:
-        _check(_lib.dmuon_expert_input_grad(d, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), dx.data_ptr(), st),
-               "dmuon_expert_input_grad")
-    return dx
+    return _expert_rows(_lib.dmuon_expert_input_grad, "dmuon_expert_input_grad", dy, w, offsets, out, stream, False)
 
 
 def dmuon_expert_weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, *,
@@ -804,24 +798,26 @@ def dmuon_expert_weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.T
     weights (experts x n x k, in x's dtype or float32), added to ``out`` with
     ``accumulate``.  Each dw[e] is a gradient for dmuon_step."""
     experts = _check_offsets(offsets)
-    d = dmuon_experts_t()
-    d.tokens, d.ld_n, d.ld_k = x.shape[0], _rows2(dy, "dy"), _rows2(x, "x")
-    d.dtype = _dtype(x)
-    _same_device(x.device, dy=dy, offsets=offsets, out=out)
-    if dy.dtype != x.dtype or dy.shape[0] != x.shape[0]:
+    tokens, n, ld_n = _rows2(dy, "dy")
+    rows, k, ld_k = _rows2(x, "x")
+    dt = x.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    if dy.dtype != dt or rows != tokens:
         raise ValueError("dy and x must share one dtype and their rows")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    call = _Launch(x.device, stream)
-    dw = out if out is not None else call.empty((experts, dy.shape[1], x.shape[1]), out_dtype or x.dtype)
-    _expert_weights(d, dw, "out")
-    if (d.experts, d.n, d.k) != (experts, dy.shape[1], x.shape[1]):
-        raise ValueError(f"out must be {experts} x {dy.shape[1]} x {x.shape[1]}")
-    d.out_dtype, d.accumulate = _dtype(dw), 1 if accumulate else 0
-    with call as st:
-        _check(_lib.dmuon_expert_weight_grad(d, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), dw.data_ptr(), st),
-               "dmuon_expert_weight_grad")
-    return dw
+    device = _gpu(x)
+    if out is None:
+        out = _result(device, stream, (experts, n, k), out_dtype or dt)
+    e, r, c, ldw, far = _rows3(out, "out")
+    if e != experts or r != n or c != k:
+        raise ValueError(f"out must be {experts} x {n} x {k}")
+    _same_device(device, dy, offsets, out)
+    d = dmuon_experts_t(tokens, n, k, ld_k, ld_n, ldw, far, experts, _DTYPES[dt], _dtype(out), 1 if accumulate else 0)
+    _launch(_lib.dmuon_expert_weight_grad, "dmuon_expert_weight_grad", device, stream, d, dy.data_ptr(), x.data_ptr(),
+            offsets.data_ptr(), out.data_ptr())
+    return out
 
 
 def _block_counts(rows: int, cols: int, block_rows: int) -> Tuple[int, int]:
@@ -829,24 +825,20 @@ def _block_counts(rows: int, cols: int, block_rows: int) -> Tuple[int, int]:
 
 
 def _blocks_desc(x: torch.Tensor, q_dtype: torch.dtype, block_rows: int) -> dmuon_blocks_t:
-    d = dmuon_blocks_t()
     if x.dim() == 3:
-        d.batch, d.rows, d.cols = x.shape
-        d.ldx, d.x_stride = _rows3(x, "x")
+        batch, rows, cols, ldx, far = _rows3(x, "x")
     else:
-        d.batch, d.ldx = 1, _rows2(x, "x")
-        d.rows, d.cols = x.shape
-    if block_rows not in (1, 128):
+        batch, far = 1, 0
+        rows, cols, ldx = _rows2(x, "x")
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    d.block_rows, d.x_dtype = block_rows, _dtype(x)
     if q_dtype not in _Q8:
         raise TypeError(f"unsupported 8-bit dtype {q_dtype}")
-    d.q_dtype = _Q8[q_dtype]
-    return d
+    return dmuon_blocks_t(batch, rows, cols, ldx, far, block_rows, _dtype(x), _Q8[q_dtype])
 
 
 def _dense(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
 
@@ -860,26 +852,23 @@ def dmuon_quantize_blocks(x: torch.Tensor, *, block_rows: int = 1, fmt: str = "e
     and scale_t are None otherwise."""
     dt = _FORMATS[fmt]
     d = _blocks_desc(x, dt, block_rows)
-    lead = tuple(x.shape[:-2])
-    call = _Launch(x.device, stream)
-    _same_device(x.device, q=q, scale=scale, qt=qt, scale_t=scale_t)
+    device = _gpu(x)
+    lead = x.shape[:-2]
 
     def pair(q, s, r, c, names):
         qs, ss = lead + (r, c), lead + _block_counts(r, c, block_rows)
-        q = _dense(q, names[0], qs, dt) if q is not None else call.empty(qs, dt)
-        s = _dense(s, names[1], ss, torch.float32) if s is not None else call.empty(ss, torch.float32)
+        q = _dense(q, names[0], qs, dt) if q is not None else _result(device, stream, qs, dt)
+        s = _dense(s, names[1], ss, torch.float32) if s is not None else _result(device, stream, ss, torch.float32)
         return q, s
 
     q, scale = pair(q, scale, d.rows, d.cols, ("q", "scale"))
     if transposed or qt is not None or scale_t is not None:
         qt, scale_t = pair(qt, scale_t, d.cols, d.rows, ("qt", "scale_t"))
-    if x.numel() == 0:
-        return q, scale, qt, scale_t
-    with call as st:
-        _check(_lib.dmuon_quantize_blocks(d, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                          qt.data_ptr() if qt is not None else None,
-                                          scale_t.data_ptr() if scale_t is not None else None, st),
-               "dmuon_quantize_blocks")
+    _same_device(device, q, scale, qt, scale_t)
+    if x.numel():
+        _launch(_lib.dmuon_quantize_blocks, "dmuon_quantize_blocks", device, stream, d, x.data_ptr(), q.data_ptr(),
+                scale.data_ptr(), qt.data_ptr() if qt is not None else None,
+                scale_t.data_ptr() if scale_t is not None else None)
     return q, scale, qt, scale_t
 
 
@@ -887,19 +876,17 @@ def dmuon_dequantize_blocks(q: torch.Tensor, scale: torch.Tensor, *, block_rows:
                             dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                             stream=None) -> torch.Tensor:
     """The values that (q, scale) of dmuon_quantize_blocks stand for."""
-    call = _Launch(q.device, stream)
-    _same_device(q.device, scale=scale, out=out)
-    x = out if out is not None else call.empty(q.shape, dtype)
+    device = _gpu(q)
+    x = out if out is not None else _result(device, stream, q.shape, dtype)
     if x.shape != q.shape:
         raise ValueError("out must have q's shape")
     d = _blocks_desc(x, q.dtype, block_rows)
     _dense(q, "q", q.shape, q.dtype)
-    _dense(scale, "scale", tuple(q.shape[:-2]) + _block_counts(d.rows, d.cols, block_rows), torch.float32)
-    if q.numel() == 0:
-        return x
-    with call as st:
-        _check(_lib.dmuon_dequantize_blocks(d, q.data_ptr(), scale.data_ptr(), x.data_ptr(), st),
-               "dmuon_dequantize_blocks")
+    _dense(scale, "scale", q.shape[:-2] + _block_counts(d.rows, d.cols, block_rows), torch.float32)
+    _same_device(device, scale, x)
+    if q.numel():
+        _launch(_lib.dmuon_dequantize_blocks, "dmuon_dequantize_blocks", device, stream, d, q.data_ptr(),
+                scale.data_ptr(), x.data_ptr())
     return x
 
 
@@ -911,40 +898,37 @@ def dmuon_block_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, 
     1 x 128 blocks, b n x k with block_rows x 128 blocks), in bfloat16 or
     float32, added to ``out`` with ``accumulate``.  With ``offsets`` b holds
     one matrix per expert (experts x n x k), as in dmuon_expert_matmul."""
-    d = dmuon_block_product_t()
-    m, k = a.shape[0], a.shape[-1]
-    d.m, d.k, d.lda = m, k, _rows2(a, "a")
-    lead = ()
+    m, k, lda = _rows2(a, "a")
     if offsets is not None:
-        d.ldb, d.b_stride = _rows3(b, "b")
-        d.experts = _check_offsets(offsets, b.shape[0])
-        lead = (b.shape[0],)
+        experts, n, kb, ldb, far = _rows3(b, "b")
+        if _check_offsets(offsets) != experts:
+            raise ValueError(f"offsets must have {experts + 1} entries")
+        lead = (experts,)
     else:
-        d.ldb = _rows2(b, "b")
-    n = b.shape[-2]
-    d.n = n
-    if b.shape[-1] != k:
+        n, kb, ldb = _rows2(b, "b")
+        experts, far, lead = 0, 0, ()
+    if kb != k:
         raise ValueError("a and b must have the same number of columns")
     if a.dtype not in _Q8 or b.dtype not in _Q8:
         raise TypeError("a and b must be float8_e4m3fn or float8_e5m2")
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    d.a_dtype, d.b_dtype, d.b_block_rows = _Q8[a.dtype], _Q8[b.dtype], block_rows
-    _same_device(a.device, a_scale=a_scale, b=b, b_scale=b_scale, offsets=offsets, out=out)
     _dense(a_scale, "a_scale", _block_counts(m, k, 1), torch.float32)
     _dense(b_scale, "b_scale", lead + _block_counts(n, k, block_rows), torch.float32)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    call = _Launch(a.device, stream)
-    c = out if out is not None else call.empty((m, n), out_dtype, zero=offsets is not None)
-    if c.shape[0] != m:
-        raise ValueError(f"out must have {m} rows")
-    d.ldc, d.out_dtype, d.accumulate = _rows2(c, "out", n), _dtype(c), 1 if accumulate else 0
-    with call as st:
-        _check(_lib.dmuon_block_matmul(d, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
-                                       offsets.data_ptr() if offsets is not None else None, c.data_ptr(), st),
-               "dmuon_block_matmul")
-    return c
+    device = _gpu(a)
+    if out is None:
+        out = _result(device, stream, (m, n), out_dtype, zero=offsets is not None)
+    rows, cols, ldc = _rows2(out, "out")
+    if rows != m or cols != n:
+        raise ValueError(f"out must be {m} x {n}")
+    _same_device(device, a_scale, b, b_scale, offsets, out)
+    d = dmuon_block_product_t(m, n, k, lda, ldb, ldc, far, experts, _Q8[a.dtype], _Q8[b.dtype], block_rows, _dtype(out),
+                              1 if accumulate else 0)
+    _launch(_lib.dmuon_block_matmul, "dmuon_block_matmul", device, stream, d, a.data_ptr(), a_scale.data_ptr(),
+            b.data_ptr(), b_scale.data_ptr(), offsets.data_ptr() if offsets is not None else None, out.data_ptr())
+    return out
 
 
 def dmuon_plan_describe(shapes: Sequence[Sequence[int]], **hp) -> dict:

@@ -725,38 +725,59 @@ void launch_matmul_big(const BlockArgs& P, unsigned blocks, hipStream_t stream) 
 
 // ---- product, few rows ----------------------------------------------------------
 
-template <bool A5, bool B5, bool BROWS, bool EXACT>
+// Formats and block rows are run-time values here: the branches on them are
+// uniform, and memory bounds the kernel.
+template <bool EXACT>
+__device__ __forceinline__ f32x4_t block_product_of(const i32x8_t& fb, const i32x8_t& fa, bool a5, bool b5) {
+  if (a5) return b5 ? block_product<true, true, EXACT>(fb, fa) : block_product<true, false, EXACT>(fb, fa);
+  return b5 ? block_product<false, true, EXACT>(fb, fa) : block_product<false, false, EXACT>(fb, fa);
+}
+
+template <bool EXACT>
 struct BlockSkinny {
   const float* sa;      // of the tile's first row; kb per row
   const float* sb;      // of the tile's first column, or of its 128 columns
   int64_t kb;
+  bool a5, b5, b_rows;
 
-  template <int MB>
-  __device__ __forceinline__ void step(int s, int lane, int rows, int cols, const SkinnyFrag& b,
-                                       const SkinnyFrag (&a)[MB], f32x4_t (&acc)[MB]) const {
-    const i32x8_t fb = __builtin_bit_cast(i32x8_t, b);
-    f32x4_t w;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = 4 * (lane >> 4) + r;
-      w[r] = sb[(BROWS ? (j < cols ? j : cols - 1) : 0) * kb + s];
-    }
+  template <int MB, int NB>
+  __device__ __forceinline__ void step(int s, int lane, int rows, int cols, const SkinnyFrag (&b)[NB],
+                                       const SkinnyFrag (&a)[MB], f32x4_t (&acc)[NB][MB]) const {
+    float x[MB];
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
       const int t = 16 * m + (lane & 15);
-      const float x = sa[(t < rows ? t : rows - 1) * kb + s];
-      const f32x4_t p = block_product<A5, B5, EXACT>(fb, __builtin_bit_cast(i32x8_t, a[m]));
+      x[m] = sa[(t < rows ? t : rows - 1) * kb + s];
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(x * w[r], p[r], acc[m][r]);
+    for (int n = 0; n < NB; ++n) {
+      f32x4_t w;
+      if (b_rows) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = 16 * n + 4 * (lane >> 4) + r;
+          w[r] = sb[(j < cols ? j : cols - 1) * kb + s];
+        }
+      } else {
+        const float all = sb[s];
+        w = f32x4_t{all, all, all, all};
+      }
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const f32x4_t p = block_product_of<EXACT>(__builtin_bit_cast(i32x8_t, b[n]), __builtin_bit_cast(i32x8_t, a[m]),
+                                                  a5, b5);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[n][m][r] = fmaf(x[m] * w[r], p[r], acc[n][m][r]);
+      }
     }
   }
 };
 
-template <bool A5, bool B5, bool BROWS, int MB, int W, typename OutT>
+template <int MB, int NB, int W, typename OutT>
 __global__ void __launch_bounds__(64 * W)
-block_skinny_kernel(BlockArgs P) {
-  __shared__ __attribute__((aligned(16))) float sums[W * MB * 256];
-  const uint32_t nt = (uint32_t(P.n) + 15) / 16;
+block_skinny_kernel(BlockArgs P, int a5, int b5, int b_rows) {
+  __shared__ __attribute__((aligned(16))) float sums[W * MB * NB * 256];
+  const uint32_t nt = (uint32_t(P.n) + 16 * NB - 1) / (16 * NB);
   const uint32_t tm = blockIdx.x / nt, tn = blockIdx.x - tm * nt;
   int row0 = int(tm) * 16 * MB, end = int(P.m), e = 0;
   if (P.offsets) {
@@ -765,42 +786,43 @@ block_skinny_kernel(BlockArgs P) {
     e = g.expert;
   }
   if (row0 >= end) return;
-  const int64_t j0 = int64_t(tn) * 16, kb = (P.k + kBlk - 1) / kBlk;
-  const int64_t b_scales = BROWS ? P.n : (P.n + kBlk - 1) / kBlk;
-  BlockSkinny<A5, B5, BROWS, sizeof(OutT) == 4> op;
+  const int64_t j0 = int64_t(tn) * (16 * NB), kb = (P.k + kBlk - 1) / kBlk;
+  const int64_t b_scales = b_rows ? P.n : (P.n + kBlk - 1) / kBlk;
+  BlockSkinny<sizeof(OutT) == 4> op;
   op.sa = P.a_scale + int64_t(row0) * kb;
-  op.sb = P.b_scale + (e * b_scales + (BROWS ? j0 : j0 / kBlk)) * kb;
+  op.sb = P.b_scale + (e * b_scales + (b_rows ? j0 : j0 / kBlk)) * kb;
   op.kb = kb;
-  skinny_block<decltype(op), MB, W, OutT>(op, static_cast<const char*>(P.a) + row0 * P.lda, P.lda,
-                                          static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb, P.ldb,
-                                          static_cast<OutT*>(P.c) + row0 * P.ldc + j0, P.ldc,
-                                          end - row0 < 16 * MB ? end - row0 : 16 * MB,
-                                          int(P.n - j0 < 16 ? P.n - j0 : 16), P.k, P.vec_c, P.accumulate, sums);
+  op.a5 = a5;
+  op.b5 = b5;
+  op.b_rows = b_rows;
+  skinny_block<decltype(op), MB, NB, W, OutT>(op, static_cast<const char*>(P.a) + row0 * P.lda, P.lda,
+                                              static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb, P.ldb,
+                                              static_cast<OutT*>(P.c) + row0 * P.ldc + j0, P.ldc,
+                                              end - row0 < 16 * MB ? end - row0 : 16 * MB,
+                                              int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k, P.vec_c, P.accumulate,
+                                              sums);
 }
 
-int64_t skinny_blocks(const BlockArgs& P, int mb) {
+int64_t skinny_blocks(const BlockArgs& P, int mb, int nb) {
   const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
-  return (P.m / (16 * mb) + used) * ((P.n + 15) / 16);
+  return (P.m / (16 * mb) + used) * ((P.n + 16 * nb - 1) / (16 * nb));
 }
-template <bool A5, bool B5, bool BROWS, int MB, typename OutT>
-void launch_skinny(const BlockArgs& P, hipStream_t stream) {
-  const int64_t blocks = skinny_blocks(P, MB);
+template <int MB, int NB>
+hipError_t launch_skinny(const BlockArgs& P, int a5, int b5, int b_rows, bool f32, hipStream_t stream) {
+  const int64_t blocks = skinny_blocks(P, MB, NB);
   const dim3 grid(static_cast<unsigned>(blocks));
-  switch (skinny_waves(blocks)) {
-    case 4: hipLaunchKernelGGL((block_skinny_kernel<A5, B5, BROWS, MB, 4, OutT>), grid, dim3(256), 0, stream, P); break;
-    case 8: hipLaunchKernelGGL((block_skinny_kernel<A5, B5, BROWS, MB, 8, OutT>), grid, dim3(512), 0, stream, P); break;
-    default: hipLaunchKernelGGL((block_skinny_kernel<A5, B5, BROWS, MB, 16, OutT>), grid, dim3(1024), 0, stream, P); break;
+  if (skinny_waves(blocks) == 8) {
+    if (f32) hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 8, float>), grid, dim3(512), 0, stream, P, a5, b5, b_rows);
+    else hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 8, uint16_t>), grid, dim3(512), 0, stream, P, a5, b5, b_rows);
+  } else {
+    if (f32) hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 16, float>), grid, dim3(1024), 0, stream, P, a5, b5, b_rows);
+    else hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 16, uint16_t>), grid, dim3(1024), 0, stream, P, a5, b5, b_rows);
   }
+  return hipGetLastError();
 }
 
 template <bool A5, bool B5, bool BROWS, typename OutT>
 void launch_matmul(const BlockArgs& P, bool vec, dim3 grid, hipStream_t stream) {
-  // at most 16, or 32, rows per expert on average
-  const int64_t experts = P.offsets ? P.experts : 1;
-  if (vec && skinny_blocks(P, 1) <= kMaxSkinnyBlocks) {
-    if (P.m <= 16 * experts) return launch_skinny<A5, B5, BROWS, 1, OutT>(P, stream);
-    if (P.m <= 32 * experts) return launch_skinny<A5, B5, BROWS, 2, OutT>(P, stream);
-  }
   if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, OutT>), grid, dim3(kThreads), 0, stream, P);
   else hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, false, OutT>), grid, dim3(kThreads), 0, stream, P);
 }
@@ -845,8 +867,7 @@ hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, boo
   const int64_t big = (P.m / kBig + used) * ((P.n + kBig - 1) / kBig);
   // offsets of a tile's rows within 31 bits
   const bool fits = P.lda <= kMaxBigPitch && P.ldb <= kMaxBigPitch && P.experts <= kBigExperts;
-  const bool few = P.m <= 32 * int64_t(P.offsets ? P.experts : 1);
-  if (vec && !f32 && fits && big >= 128 && !few) {
+  if (vec && !f32 && fits && big >= 128) {
     const unsigned blocks = static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks);
     const int which = (a_dtype == DT_E5M2 ? 4 : 0) + (b_dtype == DT_E5M2 ? 2 : 0) + (brows ? 1 : 0);
     switch (which) {
@@ -860,6 +881,16 @@ hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, boo
       default: launch_matmul_big<true, true, true>(P, blocks, stream); break;
     }
     return hipGetLastError();
+  }
+  const int a5 = a_dtype == DT_E5M2, b5 = b_dtype == DT_E5M2;
+  if (vec && skinny_blocks(P, 1, 1) <= kMaxSkinnyBlocks) {
+    // at most 16, or 32, rows per expert on average
+    const int64_t experts = P.offsets ? P.experts : 1;
+    if (P.m <= 16 * experts) {
+      if (skinny_blocks(P, 1, 2) >= kSkinnyWide) return launch_skinny<1, 2>(P, a5, b5, brows, f32, stream);
+      return launch_skinny<1, 1>(P, a5, b5, brows, f32, stream);
+    }
+    if (P.m <= 32 * experts) return launch_skinny<2, 2>(P, a5, b5, brows, f32, stream);
   }
   const int64_t nt = (P.n + kBlk - 1) / kBlk;
   const dim3 grid(static_cast<unsigned>(grouped_grid((P.m / kBlk + used) * nt)));

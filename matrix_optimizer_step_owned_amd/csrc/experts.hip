@@ -287,49 +287,50 @@ expert_bf16_big_kernel(ExpertArgs P) {
 // ---- bf16, few rows per expert (forward) ---------------------------------------
 
 struct ExpertSkinny {
-  template <int MB>
-  __device__ __forceinline__ void step(int, int, int, int, const SkinnyFrag& b, const SkinnyFrag (&a)[MB],
-                                       f32x4_t (&acc)[MB]) const {
+  template <int MB, int NB>
+  __device__ __forceinline__ void step(int, int, int, int, const SkinnyFrag (&b)[NB], const SkinnyFrag (&a)[MB],
+                                       f32x4_t (&acc)[NB][MB]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
-        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b.h[h]),
-                                                         __builtin_bit_cast(bf16x8_t, a[m].h[h]), acc[m], 0, 0, 0);
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+          acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b[n].h[h]),
+                                                              __builtin_bit_cast(bf16x8_t, a[m].h[h]), acc[n][m], 0, 0, 0);
   }
 };
 
-// Row tiles of 16 MB rows by column tiles of 16.
-template <int MB, int W>
+// Row tiles of 16 MB rows by column tiles of 16 NB.
+template <int MB, int NB, int W>
 __global__ void __launch_bounds__(64 * W)
 expert_skinny_kernel(ExpertArgs P) {
-  __shared__ __attribute__((aligned(16))) float sums[W * MB * 256];
-  const uint32_t nt = (uint32_t(P.n) + 15) / 16;
+  __shared__ __attribute__((aligned(16))) float sums[W * MB * NB * 256];
+  const uint32_t nt = (uint32_t(P.n) + 16 * NB - 1) / (16 * NB);
   const uint32_t tm = blockIdx.x / nt, tn = blockIdx.x - tm * nt;
   int row0;
   const GroupSpan g = group_of_tile(P.offsets, P.experts, P.tokens, 16 * MB, tm, &row0);
   if (row0 >= g.end) return;                // past the last tile
-  const int64_t j0 = int64_t(tn) * 16;
-  skinny_block<ExpertSkinny, MB, W, uint16_t>(
+  const int64_t j0 = int64_t(tn) * (16 * NB);
+  skinny_block<ExpertSkinny, MB, NB, W, uint16_t>(
       ExpertSkinny{}, static_cast<const char*>(P.a) + row0 * P.ld_k * 2, P.ld_k * 2,
       static_cast<const char*>(P.b) + (g.expert * P.w_stride + j0 * P.ldw) * 2, P.ldw * 2,
       static_cast<uint16_t*>(P.c) + row0 * P.ld_n + j0, P.ld_n, g.end - row0 < 16 * MB ? g.end - row0 : 16 * MB,
-      int(P.n - j0 < 16 ? P.n - j0 : 16), P.k * 2, P.vec_c, false, sums);
+      int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k * 2, P.vec_c, false, sums);
 }
 
-int64_t skinny_blocks(const ExpertArgs& P, int mb) {
+int64_t skinny_blocks(const ExpertArgs& P, int mb, int nb) {
   const int64_t used = P.experts < P.tokens ? P.experts : P.tokens;
-  return (P.tokens / (16 * mb) + used) * ((P.n + 15) / 16);
+  return (P.tokens / (16 * mb) + used) * ((P.n + 16 * nb - 1) / (16 * nb));
 }
-template <int MB>
+template <int MB, int NB>
 hipError_t launch_skinny(const ExpertArgs& P, hipStream_t stream) {
-  const int64_t blocks = skinny_blocks(P, MB);
+  const int64_t blocks = skinny_blocks(P, MB, NB);
   const dim3 grid(static_cast<unsigned>(blocks));
-  switch (skinny_waves(blocks)) {
-    case 4: hipLaunchKernelGGL((expert_skinny_kernel<MB, 4>), grid, dim3(256), 0, stream, P); break;
-    case 8: hipLaunchKernelGGL((expert_skinny_kernel<MB, 8>), grid, dim3(512), 0, stream, P); break;
-    default: hipLaunchKernelGGL((expert_skinny_kernel<MB, 16>), grid, dim3(1024), 0, stream, P); break;
-  }
+  if (skinny_waves(blocks) == 8)
+    hipLaunchKernelGGL((expert_skinny_kernel<MB, NB, 8>), grid, dim3(512), 0, stream, P);
+  else
+    hipLaunchKernelGGL((expert_skinny_kernel<MB, NB, 16>), grid, dim3(1024), 0, stream, P);
   return hipGetLastError();
 }
 
@@ -449,13 +450,6 @@ int64_t tile_bound(const ExpertArgs& P, int64_t t) {
 
 template <int OP>
 hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hipStream_t stream) {
-  if constexpr (OP == OP_FORWARD) {
-    // at most 16, or 32, rows per expert on average
-    if (dtype == DT_BF16 && vec && skinny_blocks(P, 1) <= kMaxSkinnyBlocks) {
-      if (P.tokens <= 16 * int64_t(P.experts)) return launch_skinny<1>(P, stream);
-      if (P.tokens <= 32 * int64_t(P.experts)) return launch_skinny<2>(P, stream);
-    }
-  }
   const int64_t big = tile_bound<OP>(P, kBig);
   if (dtype == DT_BF16 && vec && big >= 128 && P.experts <= kBigExperts) {
     const dim3 grid(static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks)), block(kBigThreads);
@@ -467,6 +461,19 @@ hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hi
     }
     hipLaunchKernelGGL((expert_bf16_big_kernel<OP, uint16_t>), grid, block, 0, stream, P);
     return hipGetLastError();
+  }
+  if constexpr (OP == OP_FORWARD) {
+    // too few tiles to fill the GPU and at most 16, or 32, rows per expert on
+    // average: one 4096 x 4096 expert takes 54 us for 4 rows in 128-tiles,
+    // 5 us here; with 448 tiles (8 experts of 14336 x 4096) the tiles are
+    // faster from 2 rows per expert on
+    if (dtype == DT_BF16 && vec && skinny_blocks(P, 1, 1) <= kMaxSkinnyBlocks) {
+      if (P.tokens <= 16 * int64_t(P.experts)) {
+        if (skinny_blocks(P, 1, 2) >= kSkinnyWide) return launch_skinny<1, 2>(P, stream);
+        return launch_skinny<1, 1>(P, stream);
+      }
+      if (P.tokens <= 32 * int64_t(P.experts)) return launch_skinny<2, 2>(P, stream);
+    }
   }
   const int64_t tiles = tile_bound<OP>(P, kTile);
   const dim3 grid(static_cast<unsigned>(grouped_grid(tiles))), block(kThreads);

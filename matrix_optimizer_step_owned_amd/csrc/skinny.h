@@ -3,7 +3,7 @@
 // contiguous k, bf16 or 8-bit blocks.
 //
 // The weights are read once and bound everything, so nothing is staged: a block
-// takes 16 rows of B, its W waves split k between them, and a lane loads its
+// takes 16 NB rows of B, its W waves split k between them, and a lane loads its
 // fragment of a matrix instruction straight into registers, 32 of the 128
 // bytes that a row has in one step (two 16-byte loads; the four lanes of a row
 // take whole lines).  Four steps are in flight per wave.  A comes from L2.  The
@@ -33,19 +33,26 @@ __device__ __forceinline__ SkinnyFrag skinny_load(const char* p, int g, int left
 
 // Op: kBytes steps: multiply(a, b, acc) adds one step's product of two fragments
 // for bf16; for blocks, scales(...) and a scaled multiply.  See the two uses.
-template <class Op, int MB, int W, typename OutT>
+template <class Op, int MB, int NB, int W, typename OutT>
 __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_t lda, const char* b, int64_t ldb,
                                              OutT* c, int64_t ldc, int rows, int cols, int64_t row_bytes, bool vec_c,
                                              bool accumulate, float* sums) {
   constexpr int U = 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  f32x4_t acc[MB];
+  f32x4_t acc[NB][MB];
 #pragma unroll
-  for (int m = 0; m < MB; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int steps = int((row_bytes + 127) / 128);
   // rows past the end read the last one: their results are not stored
-  const char* bp = b + (r < cols ? r : cols - 1) * ldb;
+  const char* bp[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int j = 16 * n + r;
+    bp[n] = b + (j < cols ? j : cols - 1) * ldb;
+  }
   const char* ap[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
@@ -53,39 +60,36 @@ __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_
     ap[m] = a + (t < rows ? t : rows - 1) * lda;
   }
   for (int s0 = wave * U; s0 < steps; s0 += W * U) {
-    SkinnyFrag fb[U], fa[U][MB];
+    SkinnyFrag fb[U][NB], fa[U][MB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t at = int64_t(s0 + u) * 128;
       const int64_t rest = row_bytes - at;
       const int left = rest < 0 ? 0 : rest > 128 ? 128 : int(rest);
-      fb[u] = skinny_load(bp + at, g, left);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) fb[u][n] = skinny_load(bp[n] + at, g, left);
 #pragma unroll
       for (int m = 0; m < MB; ++m) fa[u][m] = skinny_load(ap[m] + at, g, left);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (s0 + u < steps) op.template step<MB>(s0 + u, lane, rows, cols, fb[u], fa[u], acc);
+      if (s0 + u < steps) op.template step<MB, NB>(s0 + u, lane, rows, cols, fb[u], fa[u], acc);
     }
   }
-  if constexpr (W > 1) {
 #pragma unroll
-    for (int m = 0; m < MB; ++m) *reinterpret_cast<f32x4_t*>(sums + ((wave * MB + m) * 64 + lane) * 4) = acc[m];
-    __syncthreads();
-  }
-  for (int m = wave; m < MB; m += W) {
-    f32x4_t v;
-    if constexpr (W > 1) {
-      v = *reinterpret_cast<const f32x4_t*>(sums + (m * 64 + lane) * 4);
+  for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int w = 1; w < W; ++w) v += *reinterpret_cast<const f32x4_t*>(sums + ((w * MB + m) * 64 + lane) * 4);
-    } else {
-      v = acc[0];
-    }
-    const int t = 16 * m + r;
+    for (int m = 0; m < MB; ++m)
+      *reinterpret_cast<f32x4_t*>(sums + ((wave * NB * MB + n * MB + m) * 64 + lane) * 4) = acc[n][m];
+  __syncthreads();
+  for (int q = wave; q < NB * MB; q += W) {
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(sums + (q * 64 + lane) * 4);
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += *reinterpret_cast<const f32x4_t*>(sums + ((w * NB * MB + q) * 64 + lane) * 4);
+    const int n = q / MB, t = 16 * (q % MB) + r;
     if (t < rows) {
       const float x[4] = {v[0], v[1], v[2], v[3]};
-      store4<OutT>(c + t * ldc, 4 * g, cols, vec_c, accumulate, x);
+      store4<OutT>(c + t * ldc, 16 * n + 4 * g, cols, vec_c, accumulate, x);
     }
   }
 }
@@ -93,7 +97,12 @@ __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_
 // Blocks of one launch: fewer than 2^32 threads.
 constexpr int64_t kMaxSkinnyBlocks = int64_t(1) << 23;
 
-// Waves per block: enough that the launch holds about four waves per SIMD.
-inline int skinny_waves(int64_t blocks) { return blocks >= 512 ? 4 : blocks >= 256 ? 8 : 16; }
+// Two blocks of 16 columns per block halve the reads of A, which come from L2
+// but take the same load path as the weights; worth it while enough blocks remain.
+constexpr int64_t kSkinnyWide = 256;
+
+// Waves per block (measured: 7 x 14336 x 4096 in 8 bits, 448 blocks: 15.2 us with
+// eight waves, 15.7 with four; 64 blocks of 16 waves 6.3 us).
+inline int skinny_waves(int64_t blocks) { return blocks >= 256 ? 8 : 16; }
 
 }  // namespace dmuon
