@@ -249,23 +249,25 @@ dequantize_kernel(QuantArgs P) {
 // ---- product ----------------------------------------------------------------
 
 constexpr int kThreads = 256;
-constexpr int kOpBytes = kBlk * kBlk;     // one operand's stage: 128 rows x 128 k
 
-template <bool VEC>
+// One thread's share of an operand's stage of 128 k: TILE / 32 chunks.
+template <int TILE, bool VEC>
 __device__ __forceinline__ void load_stage(const char* base, int64_t ld, int rows, int64_t k0, int64_t k,
-                                           u32x4_t (&v)[4]) {
+                                           u32x4_t (&v)[TILE / 32]) {
   const int t = threadIdx.x;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < TILE / 32; ++q) {
     const int r = (t >> 3) + 32 * q, c = (t & 7) * 16;
     const int64_t left = k - k0 - c;
     v[q] = load_chunk<1, VEC>(base + r * ld + k0 + c, r < rows ? int(left > 16 ? 16 : left) : 0);
   }
 }
-__device__ __forceinline__ void write_stage(char* lds, const u32x4_t (&v)[4]) {
+template <int TILE>
+__device__ __forceinline__ void write_stage(char* lds, const u32x4_t (&v)[TILE / 32]) {
   const int t = threadIdx.x;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) *reinterpret_cast<u32x4_t*>(lds + row_slot((t >> 3) + 32 * q, t & 7)) = v[q];
+  for (int q = 0; q < TILE / 32; ++q)
+    *reinterpret_cast<u32x4_t*>(lds + row_slot((t >> 3) + 32 * q, t & 7)) = v[q];
 }
 // A lane's 32 bytes of row r0 + lane % 16: chunks lane / 16 and lane / 16 + 4.
 // Which k a lane holds does not matter as long as both operands agree.
@@ -312,104 +314,141 @@ __device__ __forceinline__ f32x4_t block_product(const i32x8_t& fb, const i32x8_
   return p;
 }
 
-template <bool A5, bool B5, bool BROWS, bool VEC, typename OutT>
-__global__ void __launch_bounds__(kThreads)
+// Tiles of 128 or 64, four waves in 2 x 2, operands staged through registers
+// (one stage in flight, four with 64-tiles: a second one of the larger tile
+// costs the two blocks per CU that its registers allow) and a two-slot LDS
+// ring; any alignment.
+template <bool A5, bool B5, bool BROWS, bool VEC, int TILE, typename OutT>
+__global__ void __launch_bounds__(kThreads, 2)
 block_matmul_kernel(BlockArgs P) {
   constexpr bool EXACT = sizeof(OutT) == 4;
-  __shared__ __attribute__((aligned(1024))) char smem[4 * kOpBytes];
-  __shared__ float scales[2][2 * kBlk];     // A's 128 rows, B's 128 rows
-  const uint32_t nt = (uint32_t(P.n) + kBlk - 1) / kBlk;
+  constexpr int OPB = TILE * kBlk, D = TILE == 64 ? 4 : 1, F = TILE / 32;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * OPB];
+  __shared__ __attribute__((aligned(16))) float scales[2][2 * TILE];     // A's rows, B's rows
+  const uint32_t nt = (uint32_t(P.n) + TILE - 1) / TILE;
   uint32_t mt;
-  if (P.offsets) mt = group_tiles(P.offsets, P.experts, int(P.m), kBlk);
-  else mt = (uint32_t(P.m) + kBlk - 1) / kBlk;
+  if (P.offsets) mt = group_tiles(P.offsets, P.experts, int(P.m), TILE);
+  else mt = (uint32_t(P.m) + TILE - 1) / TILE;
   const uint32_t pos = xcd_position(blockIdx.x, mt * nt);
   if (pos >= mt * nt) return;
   int tm, tn, row0, end, e = 0;
   tile_of_position(pos, mt, nt, &tm, &tn);
   if (P.offsets) {
-    const GroupSpan g = group_of_tile(P.offsets, P.experts, int(P.m), kBlk, tm, &row0);
+    const GroupSpan g = group_of_tile(P.offsets, P.experts, int(P.m), TILE, tm, &row0);
     end = g.end;
     e = g.expert;
   } else {
-    row0 = tm * kBlk;
+    row0 = tm * TILE;
     end = int(P.m);
   }
-  const int64_t j0 = int64_t(tn) * kBlk;
-  const int rows = end - row0 < kBlk ? end - row0 : kBlk;
-  const int cols = int(P.n - j0 < kBlk ? P.n - j0 : kBlk);
-  const int64_t kb = (P.k + kBlk - 1) / kBlk;
+  const int64_t j0 = int64_t(tn) * TILE;
+  const int rows = end - row0 < TILE ? end - row0 : TILE;
+  const int cols = int(P.n - j0 < TILE ? P.n - j0 : TILE);
+  const int kb = int((P.k + kBlk - 1) / kBlk);
   const char* a = static_cast<const char*>(P.a) + row0 * P.lda;
   const char* b = static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb;
-  // this thread's scale of a stage: threads 0-127 A's rows, 128-255 B's
+  // this thread's scale of a stage: the first TILE threads A's rows, the next B's
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const float* sp = nullptr;
-  if (t < kBlk) {
+  if (t < TILE) {
     if (t < rows) sp = P.a_scale + (int64_t(row0) + t) * kb;
-  } else if (t - kBlk < cols) {
-    const int64_t brows = BROWS ? P.n : int64_t(nt);
-    sp = P.b_scale + (e * brows + (BROWS ? j0 + t - kBlk : tn)) * kb;
+  } else if (t - TILE < cols && t < 2 * TILE) {
+    const int64_t brows = BROWS ? P.n : (P.n + kBlk - 1) / kBlk;
+    sp = P.b_scale + (e * brows + (BROWS ? j0 + t - TILE : j0 / kBlk)) * kb;
   }
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  f32x4_t acc[4][4];
+  const int wm = (wave >> 1) * (TILE / 2), wn = (wave & 1) * (TILE / 2);
+  f32x4_t acc[F][F];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  u32x4_t va[4], vb[4];
-  float vs = 0.f;
-  load_stage<VEC>(a, P.lda, rows, 0, P.k, va);
-  load_stage<VEC>(b, P.ldb, cols, 0, P.k, vb);
-  if (sp) vs = sp[0];
-  write_stage(smem, va);
-  write_stage(smem + kOpBytes, vb);
-  scales[0][t] = vs;
-  if (kb > 1) {
-    load_stage<VEC>(a, P.lda, rows, kBlk, P.k, va);
-    load_stage<VEC>(b, P.ldb, cols, kBlk, P.k, vb);
-    if (sp) vs = sp[1];
-  }
-  for (int64_t st = 0; st < kb; ++st) {
-    char* cur = smem + (st & 1) * 2 * kOpBytes;
-    char* nxt = smem + ((st + 1) & 1) * 2 * kOpBytes;
-    const float* sc = scales[st & 1];
-    __syncthreads();
-    if (st + 1 < kb) {
-      write_stage(nxt, va);
-      write_stage(nxt + kOpBytes, vb);
-      scales[(st + 1) & 1][t] = vs;
-      if (st + 2 < kb) {
-        load_stage<VEC>(a, P.lda, rows, (st + 2) * kBlk, P.k, va);
-        load_stage<VEC>(b, P.ldb, cols, (st + 2) * kBlk, P.k, vb);
-        if (sp) vs = sp[st + 2];
+    for (int j = 0; j < F; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  u32x4_t va[D][TILE / 32], vb[D][TILE / 32];
+  float vs[D];
+  auto load = [&](int st, int d) {
+    if (st < kb) {
+      load_stage<TILE, VEC>(a, P.lda, rows, int64_t(st) * kBlk, P.k, va[d]);
+      load_stage<TILE, VEC>(b, P.ldb, cols, int64_t(st) * kBlk, P.k, vb[d]);
+      vs[d] = sp ? sp[st] : 0.f;
+    }
+  };
+  auto write = [&](int st, int d) {
+    if (st < kb) {
+      write_stage<TILE>(smem + (st & 1) * 2 * OPB, va[d]);
+      write_stage<TILE>(smem + (st & 1) * 2 * OPB + OPB, vb[d]);
+      if (t < 2 * TILE) scales[st & 1][t] = vs[d];
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  write(0, 0);
+  load(D, 0);
+  for (int base = 0; base < kb; base += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int st = base + d;
+      if (st >= kb) break;
+      const char* cur = smem + (st & 1) * 2 * OPB;
+      const float* sc = scales[st & 1];
+      __syncthreads();
+      write(st + 1, (d + 1) % D);
+      load(st + 1 + D, (d + 1) % D);
+      f32x4_t sb[F];
+      if constexpr (BROWS) {
+#pragma unroll
+        for (int j = 0; j < F; ++j) sb[j] = *reinterpret_cast<const f32x4_t*>(sc + TILE + wn + 16 * j + 4 * (lane >> 4));
+      }
+      float sa[F];
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        sa[i] = sc[wm + 16 * i + (lane & 15)];
+        if constexpr (!BROWS) sa[i] *= sc[TILE];   // the tile's columns share one scale
+      }
+      auto add = [&](int i, int j, const f32x4_t& p) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(BROWS ? sa[i] * sb[j][r] : sa[i], p[r], acc[i][j][r]);
+      };
+      i32x8_t fb[F];
+#pragma unroll
+      for (int j = 0; j < F; ++j) fb[j] = read_frag(cur + OPB, wn + 16 * j);
+      if constexpr (EXACT) {
+        // every fragment is widened once
+        bf16x8_t wb[F][4];
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) wb[j][q] = widen8<B5>(fb[j], q);
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          const i32x8_t fa = read_frag(cur, wm + 16 * i);
+          f32x4_t p[F];
+#pragma unroll
+          for (int j = 0; j < F; ++j) p[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const bf16x8_t wa = widen8<A5>(fa, q);
+#pragma unroll
+            for (int j = 0; j < F; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], wa, p[j], 0, 0, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < F; ++j) add(i, j, p[j]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          const i32x8_t fa = read_frag(cur, wm + 16 * i);
+#pragma unroll
+          for (int j = 0; j < F; ++j) add(i, j, block_product<A5, B5, false>(fb[j], fa));
+        }
       }
     }
-    i32x8_t fb[4];
-    f32x4_t sb[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      fb[j] = read_frag(cur + kOpBytes, wn + 16 * j);
-      if constexpr (BROWS) sb[j] = *reinterpret_cast<const f32x4_t*>(sc + kBlk + wn + 16 * j + 4 * (lane >> 4));
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const i32x8_t fa = read_frag(cur, wm + 16 * i);
-      float sa = sc[wm + 16 * i + (lane & 15)];
-      if constexpr (!BROWS) sa *= sc[kBlk];   // the tile's columns share one scale
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x4_t p = block_product<A5, B5, EXACT>(fb[j], fa);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(BROWS ? sa * sb[j][r] : sa, p[r], acc[i][j][r]);
-      }
-    }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < F; ++i) {
     const int r = wm + 16 * i + (lane & 15);
     if (r >= rows) continue;
     OutT* row = static_cast<OutT*>(P.c) + (int64_t(row0) + r) * P.ldc + j0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < F; ++j) {
       const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
       store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), cols, P.vec_c, P.accumulate, v);
     }
@@ -822,18 +861,24 @@ hipError_t launch_skinny(const BlockArgs& P, int a5, int b5, int b_rows, bool f3
 }
 
 template <bool A5, bool B5, bool BROWS, typename OutT>
-void launch_matmul(const BlockArgs& P, bool vec, dim3 grid, hipStream_t stream) {
-  if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, OutT>), grid, dim3(kThreads), 0, stream, P);
-  else hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, false, OutT>), grid, dim3(kThreads), 0, stream, P);
+void launch_matmul(const BlockArgs& P, bool vec, bool small, dim3 grid, hipStream_t stream) {
+  const dim3 block(kThreads);
+  if (small) {
+    if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, 64, OutT>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, false, 64, OutT>), grid, block, 0, stream, P);
+  } else {
+    if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, 128, OutT>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, false, 128, OutT>), grid, block, 0, stream, P);
+  }
 }
 template <bool A5, bool B5>
-void launch_matmul_fmt(const BlockArgs& P, bool brows, bool f32, bool vec, dim3 grid, hipStream_t stream) {
+void launch_matmul_fmt(const BlockArgs& P, bool brows, bool f32, bool vec, bool small, dim3 grid, hipStream_t stream) {
   if (brows) {
-    if (f32) launch_matmul<A5, B5, true, float>(P, vec, grid, stream);
-    else launch_matmul<A5, B5, true, uint16_t>(P, vec, grid, stream);
+    if (f32) launch_matmul<A5, B5, true, float>(P, vec, small, grid, stream);
+    else launch_matmul<A5, B5, true, uint16_t>(P, vec, small, grid, stream);
   } else {
-    if (f32) launch_matmul<A5, B5, false, float>(P, vec, grid, stream);
-    else launch_matmul<A5, B5, false, uint16_t>(P, vec, grid, stream);
+    if (f32) launch_matmul<A5, B5, false, float>(P, vec, small, grid, stream);
+    else launch_matmul<A5, B5, false, uint16_t>(P, vec, small, grid, stream);
   }
 }
 
@@ -892,14 +937,17 @@ hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, boo
     }
     if (P.m <= 32 * experts) return launch_skinny<2, 2>(P, a5, b5, brows, f32, stream);
   }
-  const int64_t nt = (P.n + kBlk - 1) / kBlk;
-  const dim3 grid(static_cast<unsigned>(grouped_grid((P.m / kBlk + used) * nt)));
+  // 64-tiles where 128-tiles would give fewer than two per CU: 265 x 464 x 3584
+  // takes 38 us in 128-tiles, 16 in 64-tiles
+  auto tiles = [&](int64_t t) { return (P.m / t + used) * ((P.n + t - 1) / t); };
+  const bool small = tiles(128) < 512 && tiles(64) <= kMaxSkinnyBlocks;
+  const dim3 grid(static_cast<unsigned>(grouped_grid(tiles(small ? 64 : 128))));
   if (a_dtype == DT_E5M2) {
-    if (b_dtype == DT_E5M2) launch_matmul_fmt<true, true>(P, brows, f32, vec, grid, stream);
-    else launch_matmul_fmt<true, false>(P, brows, f32, vec, grid, stream);
+    if (b_dtype == DT_E5M2) launch_matmul_fmt<true, true>(P, brows, f32, vec, small, grid, stream);
+    else launch_matmul_fmt<true, false>(P, brows, f32, vec, small, grid, stream);
   } else {
-    if (b_dtype == DT_E5M2) launch_matmul_fmt<false, true>(P, brows, f32, vec, grid, stream);
-    else launch_matmul_fmt<false, false>(P, brows, f32, vec, grid, stream);
+    if (b_dtype == DT_E5M2) launch_matmul_fmt<false, true>(P, brows, f32, vec, small, grid, stream);
+    else launch_matmul_fmt<false, false>(P, brows, f32, vec, small, grid, stream);
   }
   return hipGetLastError();
 }

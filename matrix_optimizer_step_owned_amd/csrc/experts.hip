@@ -27,9 +27,15 @@
 namespace dmuon {
 namespace {
 
-constexpr int kTile = 128;        // edge of the output tile
+constexpr int kTile = 128;        // edge of the larger tile
+constexpr int kSmallTile = 64;
 constexpr int kStage = 64;        // bf16: summed indices per LDS stage
-constexpr int kThreads = 256;     // four waves, 2 x 2 quadrants of 64 x 64
+constexpr int kThreads = 256;     // four waves, 2 x 2 quadrants of the tile
+// Stages of operands in flight in registers: four for the small tile (16
+// registers a stage), two for the larger one.  A stage's arithmetic takes
+// 0.1 to 0.5 us and a load 1 us or more, so with one stage in flight a few
+// tiles with a long sum ran at a load's latency per stage.
+constexpr int depth_of(int tile) { return tile == kTile ? 2 : 4; }
 
 // What one block works on: rows/cols of C that exist from the tile's corner
 // on, the length of the sum, and the corner's operand and result addresses.
@@ -86,22 +92,25 @@ __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int t
 
 // ---- bf16 -------------------------------------------------------------------
 
-// LDS offset of the 32-byte unit u (16 columns) of row s, rows of 128 columns:
+// LDS offset of the 32-byte unit u (16 columns) of row s, rows of TILE columns:
 // the eight rows that half a wave's transpose read touches (s & 3 and bit 3)
-// go to eight different units.
+// go to eight different pieces of the 256 bytes that the banks hold.
+template <int TILE>
 __device__ __forceinline__ int col_slot(int s, int u) {
-  return s * (kTile * 2) + ((u ^ ((s & 3) | ((s >> 1) & 4))) << 5);
+  if constexpr (TILE == 128) return s * 256 + ((u ^ ((s & 3) | ((s >> 1) & 4))) << 5);
+  else return s * 128 + ((u ^ (((s >> 1) & 1) | ((s >> 2) & 2))) << 5);
 }
 
-// One thread's share of an operand's stage: four 16-byte chunks.
-template <bool COLS, bool VEC>
+// One thread's share of an operand's stage: TILE / 32 chunks of 16 bytes.
+template <int TILE, bool COLS, bool VEC>
 __device__ __forceinline__ void load_stage(const char* base, int64_t ld, int extent, int s0, int sum,
-                                           u32x4_t (&v)[4]) {
+                                           u32x4_t (&v)[TILE / 32]) {
   const int t = threadIdx.x;
+  constexpr int PER = TILE / 8;          // chunks per row of columns
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < TILE / 32; ++q) {
     if constexpr (COLS) {   // row s, columns 8c..
-      const int s = s0 + (t >> 4) + 16 * q, c = (t & 15) * 8;
+      const int s = s0 + t / PER + kThreads / PER * q, c = (t % PER) * 8;
       v[q] = load_chunk<2, VEC>(base + s * ld + c * 2, s < sum ? extent - c : 0);
     } else {                // row r, s 8c..
       const int r = (t >> 3) + 32 * q, c = (t & 7) * 8;
@@ -109,25 +118,26 @@ __device__ __forceinline__ void load_stage(const char* base, int64_t ld, int ext
     }
   }
 }
-template <bool COLS>
-__device__ __forceinline__ void write_stage(char* lds, const u32x4_t (&v)[4]) {
+template <int TILE, bool COLS>
+__device__ __forceinline__ void write_stage(char* lds, const u32x4_t (&v)[TILE / 32]) {
   const int t = threadIdx.x;
+  constexpr int PER = TILE / 8;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int at = COLS ? col_slot((t >> 4) + 16 * q, (t & 15) >> 1) + (t & 1) * 16
+  for (int q = 0; q < TILE / 32; ++q) {
+    const int at = COLS ? col_slot<TILE>(t / PER + kThreads / PER * q, (t % PER) >> 1) + (t & 1) * 16
                         : row_slot((t >> 3) + 32 * q, t & 7);
     *reinterpret_cast<u32x4_t*>(lds + at) = v[q];
   }
 }
 // A lane's fragment: row (or column) r0 + lane % 16, s = 32 step + 8 (lane / 16) ..
-template <bool COLS>
+template <int TILE, bool COLS>
 __device__ __forceinline__ bf16x8_t read_frag(const char* lds, int r0, int step) {
   const int lane = threadIdx.x & 63;
   if constexpr (COLS) {
     typedef short s16x4_t __attribute__((ext_vector_type(4)));
     const int s = 32 * step + 8 * (lane >> 4) + ((lane & 15) >> 2);
-    const char* p = lds + col_slot(s, r0 >> 4) + (lane & 3) * 8;
-    const char* q = lds + col_slot(s + 4, r0 >> 4) + (lane & 3) * 8;
+    const char* p = lds + col_slot<TILE>(s, r0 >> 4) + (lane & 3) * 8;
+    const char* q = lds + col_slot<TILE>(s + 4, r0 >> 4) + (lane & 3) * 8;
     union { s16x4_t h[2]; bf16x8_t v; } u;
     u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DMUON_LDS s16x4_t*)p);
     u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DMUON_LDS s16x4_t*)q);
@@ -137,67 +147,71 @@ __device__ __forceinline__ bf16x8_t read_frag(const char* lds, int r0, int step)
   }
 }
 
-template <int OP, bool VEC, typename OutT>
+template <int OP, bool VEC, int TILE, typename OutT>
 __global__ void __launch_bounds__(kThreads)
 expert_bf16_kernel(ExpertArgs P) {
   constexpr bool CA = OP == OP_WEIGHT, CB = OP != OP_FORWARD;
-  constexpr int OPB = kTile * kStage * 2;
+  constexpr int OPB = TILE * kStage * 2, D = depth_of(TILE), F = TILE / 32;
   __shared__ __attribute__((aligned(1024))) char smem[4 * OPB];
   Work w;
-  if (!find_work<OP>(P, kTile, kTile, 2, sizeof(OutT), &w)) return;
+  if (!find_work<OP>(P, TILE, TILE, 2, sizeof(OutT), &w)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  f32x4_t acc[4][4];
+  const int wm = (wave >> 1) * (TILE / 2), wn = (wave & 1) * (TILE / 2);
+  f32x4_t acc[F][F];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < F; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int stages = (w.sum + kStage - 1) / kStage;
-  u32x4_t va[4], vb[4];
-  if (stages > 0) {
-    load_stage<CA, VEC>(w.a, w.lda, w.rows, 0, w.sum, va);
-    load_stage<CB, VEC>(w.b, w.ldb, w.cols, 0, w.sum, vb);
-    write_stage<CA>(smem, va);
-    write_stage<CB>(smem + OPB, vb);
-    if (stages > 1) {
-      load_stage<CA, VEC>(w.a, w.lda, w.rows, kStage, w.sum, va);
-      load_stage<CB, VEC>(w.b, w.ldb, w.cols, kStage, w.sum, vb);
+  u32x4_t va[D][TILE / 32], vb[D][TILE / 32];
+  auto load = [&](int st, int d) {
+    if (st < stages) {
+      load_stage<TILE, CA, VEC>(w.a, w.lda, w.rows, st * kStage, w.sum, va[d]);
+      load_stage<TILE, CB, VEC>(w.b, w.ldb, w.cols, st * kStage, w.sum, vb[d]);
     }
-  }
-  for (int st = 0; st < stages; ++st) {
-    char* cur = smem + (st & 1) * 2 * OPB;
-    char* nxt = smem + ((st + 1) & 1) * 2 * OPB;
-    __syncthreads();   // stage st is written; everyone has read stage st - 1
-    if (st + 1 < stages) {
-      write_stage<CA>(nxt, va);
-      write_stage<CB>(nxt + OPB, vb);
-      if (st + 2 < stages) {
-        load_stage<CA, VEC>(w.a, w.lda, w.rows, (st + 2) * kStage, w.sum, va);
-        load_stage<CB, VEC>(w.b, w.ldb, w.cols, (st + 2) * kStage, w.sum, vb);
+  };
+  auto write = [&](int st, int d) {
+    if (st < stages) {
+      write_stage<TILE, CA>(smem + (st & 1) * 2 * OPB, va[d]);
+      write_stage<TILE, CB>(smem + (st & 1) * 2 * OPB + OPB, vb[d]);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  write(0, 0);
+  load(D, 0);
+  for (int base = 0; base < stages; base += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int st = base + d;
+      if (st >= stages) break;
+      const char* cur = smem + (st & 1) * 2 * OPB;
+      __syncthreads();   // stage st is written; everyone has read stage st - 1
+      write(st + 1, (d + 1) % D);
+      load(st + 1 + D, (d + 1) % D);
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        bf16x8_t fa[F], fb[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) fa[i] = read_frag<TILE, CA>(cur, wm + 16 * i, step);
+#pragma unroll
+        for (int j = 0; j < F; ++j) fb[j] = read_frag<TILE, CB>(cur + OPB, wn + 16 * j, step);
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j)
+            // B first: the lane then holds row lane % 16 and four consecutive columns
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
       }
     }
-#pragma unroll
-    for (int step = 0; step < 2; ++step) {
-      bf16x8_t fa[4], fb[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i] = read_frag<CA>(cur, wm + 16 * i, step);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = read_frag<CB>(cur + OPB, wn + 16 * j, step);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          // B first: the lane then holds row lane % 16 and four consecutive columns
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < F; ++i) {
     const int r = wm + 16 * i + (lane & 15);
     if (r >= w.rows) continue;
     OutT* row = reinterpret_cast<OutT*>(w.c + r * w.ldc);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < F; ++j) {
       const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
       store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), w.cols, P.vec_c, P.accumulate, v);
     }
@@ -336,17 +350,18 @@ hipError_t launch_skinny(const ExpertArgs& P, hipStream_t stream) {
 
 // ---- fp32 -------------------------------------------------------------------
 
-constexpr int kStageF = 16;                 // summed indices per stage
-constexpr int kPitchF = kTile + 4;          // words per LDS row (one s, 128 rows)
+constexpr int kStageF = 16;                               // summed indices per stage
+constexpr int pitch_f(int tile) { return tile + 4; }      // words per LDS row (one s, TILE rows)
 
-template <bool COLS, bool VEC>
+template <int TILE, bool COLS, bool VEC>
 __device__ __forceinline__ void load_stage_f(const char* base, int64_t ld, int extent, int s0, int sum,
-                                             u32x4_t (&v)[2]) {
+                                             u32x4_t (&v)[TILE / 64]) {
   const int t = threadIdx.x;
+  constexpr int PER = TILE / 4;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < TILE / 64; ++q) {
     if constexpr (COLS) {
-      const int s = s0 + (t >> 5) + 8 * q, c = (t & 31) * 4;
+      const int s = s0 + t / PER + kThreads / PER * q, c = (t % PER) * 4;
       v[q] = load_chunk<4, VEC>(base + s * ld + c * 4, s < sum ? extent - c : 0);
     } else {
       const int r = (t >> 2) + 64 * q, c = (t & 3) * 4;
@@ -354,84 +369,89 @@ __device__ __forceinline__ void load_stage_f(const char* base, int64_t ld, int e
     }
   }
 }
-template <bool COLS>
-__device__ __forceinline__ void write_stage_f(float* lds, const u32x4_t (&v)[2]) {
+template <int TILE, bool COLS>
+__device__ __forceinline__ void write_stage_f(float* lds, const u32x4_t (&v)[TILE / 64]) {
   const int t = threadIdx.x;
+  constexpr int PER = TILE / 4;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < TILE / 64; ++q) {
     if constexpr (COLS) {
-      *reinterpret_cast<u32x4_t*>(lds + ((t >> 5) + 8 * q) * kPitchF + (t & 31) * 4) = v[q];
+      *reinterpret_cast<u32x4_t*>(lds + (t / PER + kThreads / PER * q) * pitch_f(TILE) + (t % PER) * 4) = v[q];
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        lds[((t & 3) * 4 + e) * kPitchF + (t >> 2) + 64 * q] = __uint_as_float(v[q][e]);
+        lds[((t & 3) * 4 + e) * pitch_f(TILE) + (t >> 2) + 64 * q] = __uint_as_float(v[q][e]);
     }
   }
 }
 
-template <int OP, bool VEC>
+template <int OP, bool VEC, int TILE>
 __global__ void __launch_bounds__(kThreads)
 expert_f32_kernel(ExpertArgs P) {
   constexpr bool CA = OP == OP_WEIGHT, CB = OP != OP_FORWARD;
-  constexpr int OPW = kStageF * kPitchF;
+  constexpr int OPW = kStageF * pitch_f(TILE), D = depth_of(TILE), F = TILE / 64;
   __shared__ __attribute__((aligned(16))) float smem[4 * OPW];
   Work w;
-  if (!find_work<OP>(P, kTile, kTile, 4, 4, &w)) return;
+  if (!find_work<OP>(P, TILE, TILE, 4, 4, &w)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  f32x16_t acc[2][2];
+  const int wm = (wave >> 1) * (TILE / 2), wn = (wave & 1) * (TILE / 2);
+  f32x16_t acc[F][F];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < F; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int stages = (w.sum + kStageF - 1) / kStageF;
-  u32x4_t va[2], vb[2];
-  if (stages > 0) {
-    load_stage_f<CA, VEC>(w.a, w.lda, w.rows, 0, w.sum, va);
-    load_stage_f<CB, VEC>(w.b, w.ldb, w.cols, 0, w.sum, vb);
-    write_stage_f<CA>(smem, va);
-    write_stage_f<CB>(smem + OPW, vb);
-    if (stages > 1) {
-      load_stage_f<CA, VEC>(w.a, w.lda, w.rows, kStageF, w.sum, va);
-      load_stage_f<CB, VEC>(w.b, w.ldb, w.cols, kStageF, w.sum, vb);
+  u32x4_t va[D][TILE / 64], vb[D][TILE / 64];
+  auto load = [&](int st, int d) {
+    if (st < stages) {
+      load_stage_f<TILE, CA, VEC>(w.a, w.lda, w.rows, st * kStageF, w.sum, va[d]);
+      load_stage_f<TILE, CB, VEC>(w.b, w.ldb, w.cols, st * kStageF, w.sum, vb[d]);
     }
-  }
-  for (int st = 0; st < stages; ++st) {
-    float* cur = smem + (st & 1) * 2 * OPW;
-    float* nxt = smem + ((st + 1) & 1) * 2 * OPW;
-    __syncthreads();
-    if (st + 1 < stages) {
-      write_stage_f<CA>(nxt, va);
-      write_stage_f<CB>(nxt + OPW, vb);
-      if (st + 2 < stages) {
-        load_stage_f<CA, VEC>(w.a, w.lda, w.rows, (st + 2) * kStageF, w.sum, va);
-        load_stage_f<CB, VEC>(w.b, w.ldb, w.cols, (st + 2) * kStageF, w.sum, vb);
+  };
+  auto write = [&](int st, int d) {
+    if (st < stages) {
+      write_stage_f<TILE, CA>(smem + (st & 1) * 2 * OPW, va[d]);
+      write_stage_f<TILE, CB>(smem + (st & 1) * 2 * OPW + OPW, vb[d]);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  write(0, 0);
+  load(D, 0);
+  for (int base = 0; base < stages; base += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int st = base + d;
+      if (st >= stages) break;
+      const float* cur = smem + (st & 1) * 2 * OPW;
+      __syncthreads();
+      write(st + 1, (d + 1) % D);
+      load(st + 1 + D, (d + 1) % D);
+#pragma unroll
+      for (int s = 0; s < kStageF; s += 2) {
+        float fa[F], fb[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          fa[i] = cur[(s + (lane >> 5)) * pitch_f(TILE) + wm + 32 * i + (lane & 31)];
+          fb[i] = cur[OPW + (s + (lane >> 5)) * pitch_f(TILE) + wn + 32 * i + (lane & 31)];
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
       }
     }
-#pragma unroll
-    for (int s = 0; s < kStageF; s += 2) {
-      float fa[2], fb[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fa[i] = cur[(s + (lane >> 5)) * kPitchF + wm + 32 * i + (lane & 31)];
-        fb[i] = cur[OPW + (s + (lane >> 5)) * kPitchF + wn + 32 * i + (lane & 31)];
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < F; ++i) {
     const int r = wm + 32 * i + (lane & 31);
     if (r >= w.rows) continue;
     float* row = reinterpret_cast<float*>(w.c + r * w.ldc);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < F; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
@@ -439,6 +459,28 @@ expert_f32_kernel(ExpertArgs P) {
       }
   }
 }
+
+template <int OP, int TILE>
+hipError_t launch_tiles(const ExpertArgs& P, int64_t tiles, int dtype, int out_dtype, bool vec, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(grouped_grid(tiles))), block(kThreads);
+  if (dtype == DT_F32) {
+    if (vec) hipLaunchKernelGGL((expert_f32_kernel<OP, true, TILE>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((expert_f32_kernel<OP, false, TILE>), grid, block, 0, stream, P);
+    return hipGetLastError();
+  }
+  if constexpr (OP == OP_WEIGHT) {
+    if (out_dtype == DT_F32) {
+      if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, TILE, float>), grid, block, 0, stream, P);
+      else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, TILE, float>), grid, block, 0, stream, P);
+      return hipGetLastError();
+    }
+  }
+  if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, TILE, uint16_t>), grid, block, 0, stream, P);
+  else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, TILE, uint16_t>), grid, block, 0, stream, P);
+  return hipGetLastError();
+}
+
+constexpr int64_t kMaxSmallTiles = int64_t(1) << 23;    // fewer than 2^32 threads
 
 // Tiles of edge t that any offsets could need.
 template <int OP>
@@ -475,23 +517,15 @@ hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hi
       if (P.tokens <= 32 * int64_t(P.experts)) return launch_skinny<2, 2>(P, stream);
     }
   }
-  const int64_t tiles = tile_bound<OP>(P, kTile);
-  const dim3 grid(static_cast<unsigned>(grouped_grid(tiles))), block(kThreads);
-  if (dtype == DT_F32) {
-    if (vec) hipLaunchKernelGGL((expert_f32_kernel<OP, true>), grid, block, 0, stream, P);
-    else hipLaunchKernelGGL((expert_f32_kernel<OP, false>), grid, block, 0, stream, P);
-  } else {
-    if constexpr (OP == OP_WEIGHT) {
-      if (out_dtype == DT_F32) {
-        if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, float>), grid, block, 0, stream, P);
-        else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, float>), grid, block, 0, stream, P);
-        return hipGetLastError();
-      }
-    }
-    if (vec) hipLaunchKernelGGL((expert_bf16_kernel<OP, true, uint16_t>), grid, block, 0, stream, P);
-    else hipLaunchKernelGGL((expert_bf16_kernel<OP, false, uint16_t>), grid, block, 0, stream, P);
-  }
-  return hipGetLastError();
+  // 64-tiles where 128-tiles would leave CUs idle: fewer than two per CU, or,
+  // for the weight gradient, whose tiles are as long as their experts' rows,
+  // fewer than 64 per expert.  fp32 forward of 294 rows over 64 experts of
+  // 16 x 640: 54 us in 128-tiles, 20 in 64-tiles; fp32 weight gradient of 8192
+  // skewed rows over 16 experts of 352 x 531: 196 and 96 us.
+  const int64_t tiles = tile_bound<OP>(P, kTile), small = tile_bound<OP>(P, kSmallTile);
+  const bool few = tiles < 512 || (OP == OP_WEIGHT && tiles < 64 * int64_t(P.experts));
+  if (few && small <= kMaxSmallTiles) return launch_tiles<OP, kSmallTile>(P, small, dtype, out_dtype, vec, stream);
+  return launch_tiles<OP, kTile>(P, tiles, dtype, out_dtype, vec, stream);
 }
 
 }  // namespace
