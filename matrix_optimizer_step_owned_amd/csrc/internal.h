@@ -199,7 +199,7 @@ struct QuantArgs {
   float* scale_t;
   int64_t batch, rows, cols, ldx, x_stride;
   int32_t block_rows;        // 1 or 128
-  int32_t vec_x, vec_q, vec_qt;   // whole-chunk accesses are aligned
+  int32_t vec_x;   // whole chunks of x are aligned
 };
 hipError_t launch_quantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream);
 hipError_t launch_dequantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream);

@@ -191,8 +191,6 @@ int dmuon_quantize_blocks(const dmuon_blocks_t* d, const void* x, void* q, float
   P.q = static_cast<uint8_t*>(q); P.scale = scale;
   P.qt = static_cast<uint8_t*>(qt); P.scale_t = scale_t;
   P.vec_x = aligned(x, 16) && d->cols % 8 == 0 && d->ldx * xs % 16 == 0 && (d->batch == 1 || d->x_stride * xs % 16 == 0);
-  P.vec_q = aligned(q, 8) && d->cols % 8 == 0;
-  P.vec_qt = aligned(qt, 16) && d->rows % 16 == 0;
   const hipStream_t stream = static_cast<hipStream_t>(stream_);
   return hip_status(profiled_launch(PK_QUANTIZE, 3 * n, n * (xs + (q ? 1 : 0) + (qt ? 1 : 0)), stream,
                                     [&] { return launch_quantize(P, d->x_dtype, d->q_dtype, stream); }),
