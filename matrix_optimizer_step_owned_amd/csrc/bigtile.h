@@ -1,8 +1,8 @@
 // The 256 x 256 tile loop of the expert products in bf16.
 //
 // C[i][j] = sum_s A(i, s) B(j, s), one block of four waves per CU.  A wave
-// computes 128 x 128 of the tile (16 x 16 blocks, every second one in both
-// directions), 256 accumulation registers; 256 x 256 is the smallest tile
+// computes 128 x 128 of the tile (16 x 16 blocks, of the rows every second
+// one), 256 accumulation registers; 256 x 256 is the smallest tile
 // whose operands the load path delivers as fast as the matrix cores use them
 // (64 KB per 2048 cycles of matrix instructions).  Operands stream through a
 // two-slot LDS ring (128 KB) by direct-to-LDS loads of 64 s per stage.
@@ -93,6 +93,46 @@ struct BigGroups {
   }
 };
 
+// Which tiles a block takes.  Whole rounds of the grid first, every block one
+// tile; what is left behind them is split by rows where that gives more blocks
+// something to do.  A half or a quarter of the rows needs all of B's loads and
+// so takes about 0.75 or 0.6 of a tile's time (block-scaled, 16 uneven experts
+// of 4096 x 2048, 8192 rows: 123 to 109 us together with store_pair).
+struct BigPlan {
+  uint32_t full, left, end;    // positions of whole rounds; parts behind them; past the last position
+  int split;                   // a part has 256 >> split rows
+
+  __device__ __forceinline__ void make(uint32_t tiles, bool may_split) {
+    const uint32_t grid = gridDim.x;
+    full = tiles / grid * grid;
+    left = tiles - full;
+    split = !may_split ? 0 : 4 * left <= grid ? 2 : 2 * left <= grid ? 1 : 0;
+    left <<= split;
+    end = left ? full + grid : full;
+  }
+  // False where the position has nothing.
+  __device__ __forceinline__ bool locate(uint32_t p, uint32_t* tile, int* part) const {
+    *tile = p;
+    *part = -1;               // all of the tile
+    if (p < full) return true;
+    uint32_t i = p - full;
+    if (gridDim.x == kBigBlocks) {    // dealt to the XCDs in turn, four at a time
+      const uint32_t per = kBigBlocks / kNumXcd, x = i / per, k = i % per;
+      i = ((k >> 2) * kNumXcd + x) * 4 + (k & 3);
+    }
+    *tile = full + (i >> split);
+    *part = int(i & ((1u << split) - 1));
+    return i < left;
+  }
+  // First row of a part, and its rows out of the tile's.
+  __device__ __forceinline__ int cut(int part, int* rows) const {
+    if (part < 0) return 0;
+    const int most = kBig >> split, skip = part * most;
+    *rows = *rows - skip < most ? *rows - skip : most;
+    return skip;
+  }
+};
+
 // One tile: rows / cols of C that exist from its corner on, the length of
 // the sum in elements, addresses of the corner (bytes, row strides in bytes).
 struct BigWork {
@@ -173,7 +213,7 @@ struct BigLoads {
     if constexpr (COLS) {
       range = in == 0 ? 0u : uint32_t(in - 1) * uint32_t(ld) + uint32_t(extent) * 2;
     } else {
-      range = uint32_t(extent - 1) * uint32_t(ld) + uint32_t(in) * 2;
+      range = in == 0 ? 0u : uint32_t(extent - 1) * uint32_t(ld) + uint32_t(in) * 2;
       outside = first_s < left ? 0u : kOutside;
     }
     rsrc = slab_rsrc(p, range);
@@ -243,34 +283,34 @@ __device__ __forceinline__ void clear(f32x4_t (&acc)[NI][8]) {
 #undef DMUON_ACC8
 
 // Writes one tile: the lane holds row lane % 16 and columns 4 (lane / 16) .. of
-// every block.
+// every block.  bf16 results trade words with the neighbouring sixteen lanes
+// first, so that a lane writes 16 bytes and a row's four lanes 64: with 8 bytes
+// each the L2's requests for 32 bytes bound the stores.
 template <typename OutT, int NI>
 __device__ __forceinline__ void store_tile(const BigWork& w, const f32x4_t (&acc)[NI][8], bool vec_c, bool accumulate,
                                            int wave, int lane) {
-  const int wm = wave >> 1, wn = wave & 1;
-  const int col0 = 16 * wn + 4 * (lane >> 4);
+  const int wm = wave >> 1, wn = wave & 1, g = lane >> 4;
   const bool plain = vec_c && !accumulate && w.cols == kBig;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int r = 32 * i + 16 * wm + (lane & 15);
-    OutT* row = reinterpret_cast<OutT*>(w.c + int64_t(r) * w.ldc);
-    if (r < w.rows) {
-      if (plain) {
+    OutT* row = reinterpret_cast<OutT*>(w.c + int64_t(r) * w.ldc) + 128 * wn;
+    if (plain) {
+      if constexpr (sizeof(OutT) == 4) {
+        if (r < w.rows) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if constexpr (sizeof(OutT) == 4) {
-            *reinterpret_cast<f32x4_t*>(row + col0 + 32 * j) = acc[i][j];
-          } else {
-            const u32x2_t p = {pack2_bf16(acc[i][j][0], acc[i][j][1]), pack2_bf16(acc[i][j][2], acc[i][j][3])};
-            *reinterpret_cast<u32x2_t*>(row + col0 + 32 * j) = p;
-          }
+          for (int j = 0; j < 8; ++j) *reinterpret_cast<f32x4_t*>(row + 16 * j + 4 * g) = acc[i][j];
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          store4<OutT>(row, col0 + 32 * j, w.cols, vec_c, accumulate, v);
-        }
+        for (int j = 0; j < 8; j += 2)
+          store_pair(row + 16 * j, acc[i][j], acc[i][j + 1], g, r < w.rows);
+      }
+    } else if (r < w.rows) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        store4<OutT>(row, 16 * j + 4 * g, w.cols - 128 * wn, vec_c, accumulate, v);
       }
     }
     __builtin_amdgcn_sched_barrier(0);   // one row of blocks at a time
@@ -296,7 +336,8 @@ struct BigRun {
   char* const slot1;
   const bool vec_c, accumulate;
   const int lane0, wave;
-  uint32_t pos, total;
+  uint32_t pos;
+  BigPlan plan;
   BigWork w, nw;                 // present tile, next one (sum 0: none)
   BigLoads<kA> la;               // the stage whose loads are being issued
   BigLoads<kB> lb;
@@ -310,17 +351,35 @@ struct BigRun {
   // Every tile has an even number of stages; a stage past the sum reads zeros.
   static __device__ __forceinline__ int stages_of(int sum) { return (sum + 2 * kBigStage - 1) / (2 * kBigStage) * 2; }
 
+  // Tile or part of one at position p.
+  __device__ __forceinline__ void find(uint32_t p, BigWork* t) const {
+    uint32_t tile;
+    int part;
+    if (!plan.locate(p, &tile, &part)) {
+      t->sum = 0;
+      t->rows = 0;
+      return;
+    }
+    op.find(tile, t);
+    if constexpr (Op::kShort) {
+      const int skip = plan.cut(part, &t->rows);
+      t->a += int64_t(skip) * t->lda;
+      t->c += int64_t(skip) * t->ldc;
+      if (t->rows <= 0) t->sum = t->rows = 0;
+    }
+  }
   // The block's first tile from position p on that has anything to sum.
   // Tiles without are written here: zeros, or nothing when accumulating.
   __device__ __forceinline__ void find_from(uint32_t p, BigWork* t) {
     t->sum = 0;
     t->rows = t->cols = 1;       // of no tile: loads that read nothing
-    for (; p < total; p += gridDim.x) {
-      op.find(p, t);
+    for (; p < plan.end; p += gridDim.x) {
+      find(p, t);
       to_scalar(t);
       if (t->sum > 0) break;
       if (!accumulate) store_zeros<OutT>(*t, wave, here(lane0));
       t->sum = 0;
+      t->rows = t->cols = 1;
     }
     pos = p;
   }
@@ -369,7 +428,7 @@ struct BigRun {
   template <int SET, int SLOT>
   __device__ __forceinline__ void read(int r, int lane) {
     const char* slot = SLOT ? slot1 : slot0;
-    if (r < 8) fb[SET][r] = frag<kB>(slot, kBigOp, 2 * r + (wave & 1), SET, lane);
+    if (r < 8) fb[SET][r] = frag<kB>(slot, kBigOp, 8 * (wave & 1) + r, SET, lane);
     else fa[SET][r - 8] = frag<kA>(slot, 0, 2 * (r - 8) + (wave >> 1), SET, lane);
   }
   // One quarter in a fixed order: the matrix instructions of half HALF of step
@@ -429,7 +488,7 @@ struct BigRun {
     store_tile<OutT>(w, acc, vec_c, accumulate, wave, here(lane0));
   }
   __device__ __forceinline__ void run(BigGroups* groups) {
-    total = op.start(groups);
+    plan.make(op.start(groups), Op::kShort);
     // a full round of blocks covers gridDim consecutive positions, each XCD a
     // run of them (blocks go to the XCDs in turn)
     const uint32_t grid = gridDim.x, per = grid / kNumXcd;

@@ -602,7 +602,8 @@ struct BlockBig {
   float* const sc1;
   const BigGroups* const groups;
   const int lane0, wave;
-  uint32_t mt, nt, total, pos;
+  uint32_t mt, nt, pos;
+  BigPlan plan;
   BlockTile w, nw;
   BlockStream loads;
   int kb;
@@ -619,10 +620,12 @@ struct BlockBig {
   __device__ __forceinline__ void find(uint32_t p, BlockTile* t) const {
     t->rows = 0;
     t->cols = 1;
-    if (p >= total) return;
+    uint32_t tile;
+    int part;
+    if (p >= plan.end || !plan.locate(p, &tile, &part)) return;
     const BlockArgs& P = args();
     int tm, tn, row0, end, e = 0;
-    tile_of_position(p, mt, nt, &tm, &tn);
+    tile_of_position(tile, mt, nt, &tm, &tn);
     if (P.offsets) {
       e = groups->expert_of(P.experts, tm);
       row0 = uniform(groups->rows[e]) + (tm - uniform(groups->tiles[e])) * kBig;
@@ -632,7 +635,10 @@ struct BlockBig {
       end = int(P.m);
     }
     const int64_t j0 = int64_t(tn) * kBig, n_scales = BROWS ? P.n : (P.n + kBlk - 1) / kBlk;
-    t->rows = uniform(end - row0 < kBig ? end - row0 : kBig);
+    int rows = end - row0 < kBig ? end - row0 : kBig;
+    row0 += plan.cut(part, &rows);
+    if (rows <= 0) return;
+    t->rows = uniform(rows);
     t->cols = uniform(int(P.n - j0 < kBig ? P.n - j0 : kBig));
     t->a = uniform_ptr(static_cast<const char*>(P.a) + row0 * P.lda);
     t->b = uniform_ptr(static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb);
@@ -737,23 +743,20 @@ struct BlockBig {
     const int lane = here(lane0);
     const int64_t ldc = P.ldc;
     const bool vec_c = P.vec_c, accumulate = P.accumulate;
-    const int col0 = 64 * (wave & 3) + 4 * (lane >> 4);
+    const int g = lane >> 4, col0 = 64 * (wave & 3);
     const bool plain = vec_c && !accumulate && w.cols == kBig;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = 32 * i + 16 * (wave >> 2) + (lane & 15);
-      uint16_t* row = reinterpret_cast<uint16_t*>(w.c) + int64_t(r) * ldc;
-      if (r < w.rows && plain) {
+      uint16_t* row = reinterpret_cast<uint16_t*>(w.c) + int64_t(r) * ldc + col0;
+      if (plain) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x2_t p = {pack2_bf16(acc[i][j][0], acc[i][j][1]), pack2_bf16(acc[i][j][2], acc[i][j][3])};
-          *reinterpret_cast<u32x2_t*>(row + col0 + 16 * j) = p;
-        }
+        for (int j = 0; j < 4; j += 2) store_pair(row + 16 * j, acc[i][j], acc[i][j + 1], g, r < w.rows);
       } else if (r < w.rows) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          store4<uint16_t>(row, col0 + 16 * j, w.cols, vec_c, accumulate, v);
+          store4<uint16_t>(row, 16 * j + 4 * g, w.cols - col0, vec_c, accumulate, v);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -770,7 +773,7 @@ struct BlockBig {
       } else {
         mt = (uint32_t(P.m) + kBig - 1) / kBig;
       }
-      total = mt * nt;
+      plan.make(mt * nt, true);
       loads.init(int(P.lda), int(P.ldb), int(P.k), BROWS, wave, lane0);
     }
     const uint32_t grid = gridDim.x, per = grid / kNumXcd;
