@@ -287,10 +287,10 @@ __device__ __forceinline__ void clear(f32x4_t (&acc)[NI][8]) {
 // first, so that a lane writes 16 bytes and a row's four lanes 64: with 8 bytes
 // each the L2's requests for 32 bytes bound the stores.
 template <typename OutT, int NI>
-__device__ __forceinline__ void store_tile(const BigWork& w, const f32x4_t (&acc)[NI][8], bool vec_c, bool accumulate,
+__device__ __forceinline__ void store_tile(const BigWork& w, const f32x4_t (&acc)[NI][8], bool accumulate,
                                            int wave, int lane) {
   const int wm = wave >> 1, wn = wave & 1, g = lane >> 4;
-  const bool plain = vec_c && !accumulate && w.cols == kBig;
+  const bool plain = !accumulate && w.cols == kBig;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int r = 32 * i + 16 * wm + (lane & 15);
@@ -299,7 +299,10 @@ __device__ __forceinline__ void store_tile(const BigWork& w, const f32x4_t (&acc
       if constexpr (sizeof(OutT) == 4) {
         if (r < w.rows) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) *reinterpret_cast<f32x4_t*>(row + 16 * j + 4 * g) = acc[i][j];
+          for (int j = 0; j < 8; ++j) {
+            const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            store4<OutT>(row, 16 * j + 4 * g, 128, false, v);
+          }
         }
       } else {
 #pragma unroll
@@ -310,7 +313,7 @@ __device__ __forceinline__ void store_tile(const BigWork& w, const f32x4_t (&acc
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        store4<OutT>(row, 16 * j + 4 * g, w.cols - 128 * wn, vec_c, accumulate, v);
+        store4<OutT>(row, 16 * j + 4 * g, w.cols - 128 * wn, accumulate, v);
       }
     }
     __builtin_amdgcn_sched_barrier(0);   // one row of blocks at a time
@@ -334,7 +337,7 @@ struct BigRun {
   Op& op;
   char* const slot0;
   char* const slot1;
-  const bool vec_c, accumulate;
+  const bool accumulate;
   const int lane0, wave;
   uint32_t pos;
   BigPlan plan;
@@ -344,8 +347,8 @@ struct BigRun {
   int loads_left;                // stages of its tile after it
   bf16x8_t fa[2][8], fb[2][8];   // fragments of steps 0 and 1
 
-  __device__ __forceinline__ BigRun(Op& o, char* s0, char* s1, bool vec, bool acc_)
-      : op(o), slot0(s0), slot1(s1), vec_c(vec), accumulate(acc_), lane0(threadIdx.x & 63),
+  __device__ __forceinline__ BigRun(Op& o, char* s0, char* s1, bool acc_)
+      : op(o), slot0(s0), slot1(s1), accumulate(acc_), lane0(threadIdx.x & 63),
         wave(uniform(threadIdx.x >> 6)) {}
 
   // Every tile has an even number of stages; a stage past the sum reads zeros.
@@ -485,7 +488,7 @@ struct BigRun {
       stage<NI, 1>(acc);
     }
     settle(acc);
-    store_tile<OutT>(w, acc, vec_c, accumulate, wave, here(lane0));
+    store_tile<OutT>(w, acc, accumulate, wave, here(lane0));
   }
   __device__ __forceinline__ void run(BigGroups* groups) {
     plan.make(op.start(groups), Op::kShort);

@@ -498,7 +498,7 @@ block_matmul_kernel(BlockArgs P) {
 #pragma unroll
     for (int j = 0; j < F; ++j) {
       const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), cols, P.vec_c, P.accumulate, v);
+      store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), cols, P.accumulate, v);
     }
   }
 }
@@ -742,9 +742,9 @@ struct BlockBig {
     const BlockArgs& P = args();
     const int lane = here(lane0);
     const int64_t ldc = P.ldc;
-    const bool vec_c = P.vec_c, accumulate = P.accumulate;
+    const bool accumulate = P.accumulate;
     const int g = lane >> 4, col0 = 64 * (wave & 3);
-    const bool plain = vec_c && !accumulate && w.cols == kBig;
+    const bool plain = !accumulate && w.cols == kBig;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = 32 * i + 16 * (wave >> 2) + (lane & 15);
@@ -756,7 +756,7 @@ struct BlockBig {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          store4<uint16_t>(row, 16 * j + 4 * g, w.cols - col0, vec_c, accumulate, v);
+          store4<uint16_t>(row, 16 * j + 4 * g, w.cols - col0, accumulate, v);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -889,7 +889,7 @@ block_skinny_kernel(BlockArgs P, int a5, int b5, int b_rows) {
                                               static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb, P.ldb,
                                               static_cast<OutT*>(P.c) + row0 * P.ldc + j0, P.ldc,
                                               end - row0 < 16 * MB ? end - row0 : 16 * MB,
-                                              int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k, P.vec_c, P.accumulate,
+                                              int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k, P.accumulate,
                                               sums);
 }
 

@@ -45,10 +45,24 @@ struct Work {
   char* c;
   int rows, cols, sum;
   int64_t lda, ldb, ldc;   // bytes per row as stored
+  int row0, col0;          // rows and columns of C that the tile before writes
 };
 
-template <int OP>
+// A last tile of columns that would end inside a 16-byte chunk starts a few
+// columns earlier, inside the tile before, so that it ends with a whole chunk:
+// element by element such chunks took 1.6 times as long (fp32 weight gradient
+// of 3000 rows, 1024 x 511: 138 us against 82 with 512 columns).  Returns the
+// columns gained.
+__device__ __forceinline__ int whole_chunks(const char** p, int* extent, int64_t before, int eb) {
+  const int n = 16 / eb, d = before > 0 ? (n - *extent % n) % n : 0;
+  *p -= d * eb;
+  *extent += d;
+  return d;
+}
+
+template <int OP, bool VEC>
 __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int tile_n, int eb, int out_eb, Work* w) {
+  w->row0 = w->col0 = 0;
   int tm, tn;
   if constexpr (OP == OP_WEIGHT) {
     const uint32_t mt = (uint32_t(P.n) + tile_m - 1) / tile_m, nt = (uint32_t(P.k) + tile_n - 1) / tile_n;
@@ -67,6 +81,11 @@ __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int t
     w->a = static_cast<const char*>(P.a) + g.begin * w->lda + i0 * eb;
     w->b = static_cast<const char*>(P.b) + g.begin * w->ldb + j0 * eb;
     w->c = static_cast<char*>(P.c) + e * P.w_stride * out_eb + i0 * w->ldc + j0 * out_eb;
+    if constexpr (!VEC) {
+      w->row0 = whole_chunks(&w->a, &w->rows, i0, eb);
+      w->col0 = whole_chunks(&w->b, &w->cols, j0, eb);
+      w->c -= w->row0 * w->ldc + w->col0 * out_eb;
+    }
   } else {
     const int64_t cols = OP == OP_FORWARD ? P.n : P.k;
     const uint32_t nt = (uint32_t(cols) + tile_n - 1) / tile_n;
@@ -86,6 +105,10 @@ __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int t
     w->a = static_cast<const char*>(P.a) + row0 * w->lda;
     w->b = static_cast<const char*>(P.b) + g.expert * P.w_stride * eb + (OP == OP_FORWARD ? j0 * w->ldb : j0 * eb);
     w->c = static_cast<char*>(P.c) + row0 * w->ldc + j0 * out_eb;
+    if constexpr (!VEC && OP == OP_INPUT) {
+      w->col0 = whole_chunks(&w->b, &w->cols, j0, eb);
+      w->c -= w->col0 * out_eb;
+    }
   }
   return true;
 }
@@ -154,7 +177,7 @@ expert_bf16_kernel(ExpertArgs P) {
   constexpr int OPB = TILE * kStage * 2, D = depth_of(TILE), F = TILE / 32;
   __shared__ __attribute__((aligned(1024))) char smem[4 * OPB];
   Work w;
-  if (!find_work<OP>(P, TILE, TILE, 2, sizeof(OutT), &w)) return;
+  if (!find_work<OP, VEC>(P, TILE, TILE, 2, sizeof(OutT), &w)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = (wave >> 1) * (TILE / 2), wn = (wave & 1) * (TILE / 2);
   f32x4_t acc[F][F];
@@ -208,12 +231,12 @@ expert_bf16_kernel(ExpertArgs P) {
 #pragma unroll
   for (int i = 0; i < F; ++i) {
     const int r = wm + 16 * i + (lane & 15);
-    if (r >= w.rows) continue;
+    if (r < w.row0 || r >= w.rows) continue;
     OutT* row = reinterpret_cast<OutT*>(w.c + r * w.ldc);
 #pragma unroll
     for (int j = 0; j < F; ++j) {
       const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), w.cols, P.vec_c, P.accumulate, v);
+      store4<OutT>(row, wn + 16 * j + 4 * (lane >> 4), w.cols, P.accumulate, v, w.col0);
     }
   }
 }
@@ -294,7 +317,7 @@ expert_bf16_big_kernel(ExpertArgs P) {
   __shared__ BigSlot slot0, slot1;
   __shared__ BigGroups groups;
   ExpertBig<OP, OutT> op;
-  BigRun<ExpertBig<OP, OutT>> run(op, slot0.data, slot1.data, P.vec_c, P.accumulate);
+  BigRun<ExpertBig<OP, OutT>> run(op, slot0.data, slot1.data, P.accumulate);
   run.run(&groups);
 }
 
@@ -330,7 +353,7 @@ expert_skinny_kernel(ExpertArgs P) {
       ExpertSkinny{}, static_cast<const char*>(P.a) + row0 * P.ld_k * 2, P.ld_k * 2,
       static_cast<const char*>(P.b) + (g.expert * P.w_stride + j0 * P.ldw) * 2, P.ldw * 2,
       static_cast<uint16_t*>(P.c) + row0 * P.ld_n + j0, P.ld_n, g.end - row0 < 16 * MB ? g.end - row0 : 16 * MB,
-      int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k * 2, P.vec_c, false, sums);
+      int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k * 2, false, sums);
 }
 
 int64_t skinny_blocks(const ExpertArgs& P, int mb, int nb) {
@@ -392,7 +415,7 @@ expert_f32_kernel(ExpertArgs P) {
   constexpr int OPW = kStageF * pitch_f(TILE), D = depth_of(TILE), F = TILE / 64;
   __shared__ __attribute__((aligned(16))) float smem[4 * OPW];
   Work w;
-  if (!find_work<OP>(P, TILE, TILE, 4, 4, &w)) return;
+  if (!find_work<OP, VEC>(P, TILE, TILE, 4, 4, &w)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = (wave >> 1) * (TILE / 2), wn = (wave & 1) * (TILE / 2);
   f32x16_t acc[F][F];
@@ -448,14 +471,14 @@ expert_f32_kernel(ExpertArgs P) {
 #pragma unroll
   for (int i = 0; i < F; ++i) {
     const int r = wm + 32 * i + (lane & 31);
-    if (r >= w.rows) continue;
+    if (r < w.row0 || r >= w.rows) continue;
     float* row = reinterpret_cast<float*>(w.c + r * w.ldc);
 #pragma unroll
     for (int j = 0; j < F; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-        store4<float>(row, wn + 32 * j + 8 * g + 4 * (lane >> 5), w.cols, P.vec_c, P.accumulate, v);
+        store4<float>(row, wn + 32 * j + 8 * g + 4 * (lane >> 5), w.cols, P.accumulate, v, w.col0);
       }
   }
 }
@@ -520,8 +543,9 @@ hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hi
   // 64-tiles where 128-tiles would leave CUs idle: fewer than two per CU, or,
   // for the weight gradient, whose tiles are as long as their experts' rows,
   // fewer than 64 per expert.  fp32 forward of 294 rows over 64 experts of
-  // 16 x 640: 54 us in 128-tiles, 20 in 64-tiles; fp32 weight gradient of 8192
-  // skewed rows over 16 experts of 352 x 531: 196 and 96 us.
+  // 16 x 640: 54 us in 128-tiles, 20 in 64-tiles; fp32 weight gradient of 3001
+  // uneven rows over 24 experts of 1000 x 515: 196 and 96 us before
+  // whole_chunks and store4's vectors, 72 with them.
   const int64_t tiles = tile_bound<OP>(P, kTile), small = tile_bound<OP>(P, kSmallTile);
   const bool few = tiles < 512 || (OP == OP_WEIGHT && tiles < 64 * int64_t(P.experts));
   if (few && small <= kMaxSmallTiles) return launch_tiles<OP, kSmallTile>(P, small, dtype, out_dtype, vec, stream);

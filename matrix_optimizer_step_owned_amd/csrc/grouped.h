@@ -210,7 +210,7 @@ __device__ __forceinline__ void slab_load_lds(__amdgpu_buffer_rsrc_t rsrc, char*
 // Neighbouring sixteen lanes trade words first, so that a lane writes 16 bytes
 // and a row's four lanes 64: half as many requests to the L2 as with 8 bytes
 // per lane (weight gradient of 8 experts 14336 x 4096, 8192 rows: 956 to 880 us;
-// block-scaled 8192^3: 564 to 540 us).  The row is 8-byte aligned.  Every lane of the wave has to call.
+// block-scaled 8192^3: 564 to 540 us).  Any alignment.  Every lane of the wave has to call.
 __device__ __forceinline__ void store_pair(uint16_t* row, const f32x4_t& left, const f32x4_t& right, int g, bool write) {
   uint32_t x[2], y[2];
 #pragma unroll
@@ -221,38 +221,43 @@ __device__ __forceinline__ void store_pair(uint16_t* row, const f32x4_t& left, c
     x[h] = t[0];
     y[h] = t[1];
   }
-  struct __attribute__((packed, aligned(8))) Any { u32x4_t v; };
+  struct __attribute__((packed, aligned(2))) Any { u32x4_t v; };
   if (write) reinterpret_cast<Any*>(row + 16 * (g & 1) + 8 * (g >> 1))->v = u32x4_t{x[0], x[1], y[0], y[1]};
 }
 
-// Four consecutive results of a row, columns col..col+3 of n.
+// Four consecutive results of a row, of which first..n-1 are written.  Whole groups go
+// out in one store at any element's alignment (fp32 rows of 515: 49 MB took
+// 44 us in single elements).
 template <typename OutT>
-__device__ __forceinline__ void store4(OutT* row, int col, int n, bool vec, bool accumulate, const float (&x)[4]) {
+__device__ __forceinline__ void store4(OutT* row, int col, int n, bool accumulate, const float (&x)[4],
+                                       int first = 0) {
   if (col >= n) return;
   float v[4] = {x[0], x[1], x[2], x[3]};
   OutT* p = row + col;
-  if (vec && col + 4 <= n) {
+  if (col >= first && col + 4 <= n) {
     if constexpr (sizeof(OutT) == 4) {
-      if (accumulate) {
-        const f32x4_t o = *reinterpret_cast<const f32x4_t*>(p);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] += o[r];
-      }
-      const f32x4_t w = {v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_t*>(p) = w;
+      struct __attribute__((packed, aligned(4))) Any { f32x4_t v; };
+      Any* q = reinterpret_cast<Any*>(p);
+      f32x4_t o = {v[0], v[1], v[2], v[3]};
+      if (accumulate) o += q->v;
+      q->v = o;
     } else {
+      struct __attribute__((packed, aligned(2))) Any { u32x2_t v; };
+      Any* q = reinterpret_cast<Any*>(p);
       if (accumulate) {
-        const u32x2_t o = *reinterpret_cast<const u32x2_t*>(p);
-        v[0] += bf16_lo(o[0]); v[1] += bf16_hi(o[0]); v[2] += bf16_lo(o[1]); v[3] += bf16_hi(o[1]);
+        const u32x2_t old = q->v;
+        v[0] += bf16_lo(old[0]);
+        v[1] += bf16_hi(old[0]);
+        v[2] += bf16_lo(old[1]);
+        v[3] += bf16_hi(old[1]);
       }
-      const u32x2_t w = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
-      *reinterpret_cast<u32x2_t*>(p) = w;
+      q->v = u32x2_t{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
     }
     return;
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    if (col + r >= n) break;
+    if (col + r < first || col + r >= n) continue;
     if constexpr (sizeof(OutT) == 4) {
       p[r] = accumulate ? p[r] + v[r] : v[r];
     } else {

@@ -183,7 +183,6 @@ struct ExpertArgs {
   int64_t ldw, w_stride;     // rows of one expert's weights, and between experts
   int32_t experts, tokens;
   int32_t accumulate;        // weight gradient: add to what is there
-  int32_t vec_c;             // four results of a row can be stored at once
 };
 enum { OP_FORWARD = 0, OP_INPUT = 1, OP_WEIGHT = 2 };
 // vec: every row of a and b is 16-byte aligned and a whole number of 16-byte
@@ -199,7 +198,7 @@ struct QuantArgs {
   float* scale_t;
   int64_t batch, rows, cols, ldx, x_stride;
   int32_t block_rows;        // 1 or 128
-  int32_t vec_x;   // whole chunks of x are aligned
+  int32_t vec_x;             // whole chunks of x are aligned
 };
 hipError_t launch_quantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream);
 hipError_t launch_dequantize(const QuantArgs& P, int x_dtype, int q_dtype, hipStream_t stream);
@@ -214,7 +213,6 @@ struct BlockArgs {
   int64_t m, n, k, lda, ldb, ldc, b_stride;
   int32_t experts;
   int32_t accumulate;
-  int32_t vec_c;
 };
 hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, bool brows, bool f32, bool vec,
                                hipStream_t stream);

@@ -114,8 +114,6 @@ int expert_product(int op, const dmuon_experts_t* d, const void* a, const void* 
   else if (op == OP_INPUT) vec = chunks(a, d->n, d->ld_n) && chunks(b, d->k, d->ldw);
   else vec = chunks(a, d->n, d->ld_n) && chunks(b, d->k, d->ld_k);
   if (op != OP_WEIGHT) vec = vec && (d->w_stride * sz % 16 == 0 || d->experts == 1);
-  const int64_t ldc = op == OP_FORWARD ? d->ld_n : op == OP_INPUT ? d->ld_k : d->ldw;
-  P.vec_c = aligned(c, 4 * osz) && ldc % 4 == 0 && (op != OP_WEIGHT || d->w_stride % 4 == 0 || d->experts == 1);
   const hipStream_t stream = static_cast<hipStream_t>(stream_);
   const int64_t flops = product_flops(d->tokens, d->n, d->k);
   return hip_status(profiled_launch(d->dtype == DT_F32 ? PK_EXPERT_F32 : PK_EXPERT_BF16, flops, ab + bb + cbytes, stream,
@@ -263,7 +261,6 @@ int dmuon_block_matmul(const dmuon_block_product_t* d, const void* a, const floa
   P.experts = d->experts; P.accumulate = d->accumulate;
   const bool vec = aligned(a, 16) && aligned(b, 16) && d->k % 16 == 0 && d->lda % 16 == 0 && d->ldb % 16 == 0 &&
                    (ne == 1 || d->b_stride % 16 == 0);
-  P.vec_c = aligned(c, 4 * osz) && d->ldc % 4 == 0;
   const hipStream_t stream = static_cast<hipStream_t>(stream_);
   return hip_status(profiled_launch(PK_BLOCK_MATMUL, product_flops(d->m, d->n, d->k), ab + bb + cbytes, stream,
                                     [&] {

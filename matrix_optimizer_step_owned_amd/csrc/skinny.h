@@ -35,7 +35,7 @@ __device__ __forceinline__ SkinnyFrag skinny_load(const char* p, int g, int left
 // for bf16; for blocks, scales(...) and a scaled multiply.  See the two uses.
 template <class Op, int MB, int NB, int W, typename OutT>
 __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_t lda, const char* b, int64_t ldb,
-                                             OutT* c, int64_t ldc, int rows, int cols, int64_t row_bytes, bool vec_c,
+                                             OutT* c, int64_t ldc, int rows, int cols, int64_t row_bytes,
                                              bool accumulate, float* sums) {
   constexpr int U = 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -89,7 +89,7 @@ __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_
     const int n = q / MB, t = 16 * (q % MB) + r;
     if (t < rows) {
       const float x[4] = {v[0], v[1], v[2], v[3]};
-      store4<OutT>(c + t * ldc, 16 * n + 4 * g, cols, vec_c, accumulate, x);
+      store4<OutT>(c + t * ldc, 16 * n + 4 * g, cols, accumulate, x);
     }
   }
 }
