@@ -961,9 +961,10 @@ hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, boo
                                hipStream_t stream) {
   const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
   const int64_t big = (P.m / kBig + used) * ((P.n + kBig - 1) / kBig);
-  // offsets of a tile's rows within 31 bits
+  // 256-tiles from 192 on (2048 x 4096 x 4096, 128 of them: 62 us so, 57 in
+  // 128-tiles); offsets of a tile's rows within 31 bits
   const bool fits = P.lda <= kMaxBigPitch && P.ldb <= kMaxBigPitch && P.experts <= kBigExperts;
-  if (vec && !f32 && fits && big >= 128) {
+  if (vec && !f32 && fits && big >= 192) {
     const unsigned blocks = static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks);
     const int which = (a_dtype == DT_E5M2 ? 4 : 0) + (b_dtype == DT_E5M2 ? 2 : 0) + (brows ? 1 : 0);
     switch (which) {
@@ -988,10 +989,11 @@ hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, boo
     }
     if (P.m <= 32 * experts) return launch_skinny<2, 2>(P, a5, b5, brows, f32, stream);
   }
-  // 64-tiles where 128-tiles would give fewer than two per CU: 265 x 464 x 3584
+  // 64-tiles where 128-tiles would give fewer than one per CU: 2048 x 2560 x
+  // 1000 with fp32 results takes 35 us in 128-tiles, 41 in 64-tiles; 265 x 464 x 3584
   // takes 38 us in 128-tiles, 16 in 64-tiles
   auto tiles = [&](int64_t t) { return (P.m / t + used) * ((P.n + t - 1) / t); };
-  const bool small = tiles(128) < 512 && tiles(64) <= kMaxSkinnyBlocks;
+  const bool small = tiles(128) < 256 && tiles(64) <= kMaxSkinnyBlocks;
   const dim3 grid(static_cast<unsigned>(grouped_grid(tiles(small ? 64 : 128))));
   if (a_dtype == DT_E5M2) {
     if (b_dtype == DT_E5M2) launch_matmul_fmt<true, true>(P, brows, f32, vec, small, grid, stream);
