@@ -73,6 +73,7 @@ __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int t
     const GroupSpan g = group_of_expert(P.offsets, P.experts, P.tokens, e);
     const int64_t i0 = int64_t(tm) * tile_m, j0 = int64_t(tn) * tile_n;
     w->sum = g.end - g.begin;
+    if (w->sum == 0 && P.accumulate) return false;   // left as it is
     w->rows = int(P.n - i0 < tile_m ? P.n - i0 : tile_m);
     w->cols = int(P.k - j0 < tile_n ? P.k - j0 : tile_n);
     w->lda = P.ld_n * eb;
@@ -170,6 +171,10 @@ __device__ __forceinline__ bf16x8_t read_frag(const char* lds, int r0, int step)
   }
 }
 
+// Bound by a stage's latency where tiles are few and by the LDS reads where
+// they are many (each wave reads its operands' 64 or 32 rows itself): 8 experts
+// of 1200 x 1004, 4096 rows, forward 40 us, 246 TFLOP/s; one expert of 2048 x
+// 2048, 4096 rows, 50 us, 690 TFLOP/s.
 template <int OP, bool VEC, int TILE, typename OutT>
 __global__ void __launch_bounds__(kThreads)
 expert_bf16_kernel(ExpertArgs P) {
@@ -311,6 +316,9 @@ struct ExpertBig {
   }
 };
 
+// 8192^3: 1.40 to 1.43 PFLOP/s in all three directions, the board at its power
+// cap.  8 experts of 14336 x 4096, 8192 even rows: forward 885 us, input gradient
+// 770 (long sums), weight gradient 880 (short sums).
 template <int OP, typename OutT>
 __global__ void __launch_bounds__(kBigThreads)
 expert_bf16_big_kernel(ExpertArgs P) {
@@ -408,6 +416,9 @@ __device__ __forceinline__ void write_stage_f(float* lds, const u32x4_t (&v)[TIL
   }
 }
 
+// Bound by the fp32 matrix instructions for whole tiles and long sums (weight
+// gradient of 4096 x 4096, 3000 rows: 906 us, 111 of the 154 TFLOP/s that a large
+// library product reaches), by 0.4 us per stage where a CU has one tile.
 template <int OP, bool VEC, int TILE>
 __global__ void __launch_bounds__(kThreads)
 expert_f32_kernel(ExpertArgs P) {

@@ -187,6 +187,22 @@ def test_more_experts_than_the_large_tiles_hold(lib):
            oe.expert_weight_grad(a(DY), a(X), off), 1, False, "dw")
 
 
+@pytest.mark.parametrize("dtype,n,k", [(BF, 2048, 2048), (BF, 72, 40), (F32, 65, 33)])
+def test_accumulate_leaves_experts_without_rows(lib, dtype, n, k):
+    """Bit for bit, a negative zero among them."""
+    rng = np.random.default_rng(36)
+    x, dy = normal(rng, (20, k), dtype), normal(rng, (20, n), dtype)
+    dw = torch.full((4, n, k), -0.0, dtype=dtype, device=DEV)
+    dw[2, 0, 0] = float("inf")
+    offs = torch.tensor([0, 0, 7, 7, 20], dtype=torch.int32, device=DEV)
+    lib.dmuon_expert_weight_grad(dy, x, offs, out=dw, accumulate=True)
+    assert bool(torch.signbit(dw[0]).all()) and bool(torch.isinf(dw[2, 0, 0]))
+    dw[2, 0, 0] = -0.0
+    assert bool(torch.signbit(dw[2]).all())
+    lib.dmuon_expert_weight_grad(dy, x, offs, out=dw)
+    assert not bool(dw[0].any()) and not bool(dw[2].any()) and bool(dw[1].any())
+
+
 def test_concurrent_callers(lib):
     """Four threads with a stream each: every result equals the one of the
     same call made alone."""
