@@ -66,7 +66,7 @@ __device__ __forceinline__ bool find_work(const ExpertArgs& P, int tile_m, int t
   int tm, tn;
   if constexpr (OP == OP_WEIGHT) {
     const uint32_t mt = (uint32_t(P.n) + tile_m - 1) / tile_m, nt = (uint32_t(P.k) + tile_n - 1) / tile_n;
-    const uint32_t total = mt * nt * P.experts, pos = xcd_position(blockIdx.x, total);
+    const uint32_t total = mt * nt * P.experts, pos = xcd_position(blockIdx.x, mt * nt);
     if (pos >= total) return false;
     const uint32_t e = pos / (mt * nt);
     tile_of_position(pos - e * mt * nt, mt, nt, &tm, &tn);

@@ -127,10 +127,13 @@ __device__ __forceinline__ GroupSpan group_of_expert(const int32_t* offsets, int
 // Block -> position in the tile order (fewer than 2^31 tiles).  The hardware
 // deals blocks to the 8 XCDs in turn; runs of up to 32 consecutive tiles (as
 // many blocks as an XCD runs at once) go to one XCD, so that they share
-// operand panels in its L2.  Positions past `total` are idle blocks; a grid of
-// grouped_grid(bound) blocks reaches every position below any total <= bound.
-__device__ __forceinline__ uint32_t xcd_position(uint32_t block, uint32_t total) {
-  uint32_t run = (total + kNumXcd - 1) / kNumXcd;
+// operand panels in its L2.  Of every `even` consecutive tiles each XCD gets its
+// share: all tiles, or those of one expert where experts' tiles differ in
+// length (fp32 weight gradient of 24 very uneven experts of 1000 x 515, 3001 rows:
+// 76 to 69 us).  A grid of grouped_grid(bound) blocks reaches every position below any
+// total <= bound; blocks past the total are idle.
+__device__ __forceinline__ uint32_t xcd_position(uint32_t block, uint32_t even) {
+  uint32_t run = (even + kNumXcd - 1) / kNumXcd;
   if (run > 32) run = 32;
   if (run < 1) run = 1;
   const uint32_t x = block % kNumXcd, s = block / kNumXcd;
