@@ -685,7 +685,13 @@ _Q8 = {torch.float8_e4m3fn: DMUON_E4M3, torch.float8_e5m2: DMUON_E5M2}
 _FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current stream's handle without a Stream object; a private name of
+# PyTorch that its builds without a GPU backend lack.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _launch(f, name: str, device, stream, *args) -> None:
