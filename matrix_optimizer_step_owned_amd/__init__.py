@@ -713,6 +713,16 @@ def _gpu(t: torch.Tensor):
     return t.device
 
 
+def _no_graph(name: str, *tensors) -> None:
+    """Refuses a call that autograd would have to record: the library records
+    no graph, so the result's gradient would be lost in silence."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} records no graph, and a tensor requires a gradient: call it under "
+                                 "torch.no_grad() or on detached tensors")
+
+
 def _result(device, stream, shape, dtype, zero=False) -> torch.Tensor:
     """A result allocated here: it belongs to the stream the call runs on (see
     _workspace)."""
@@ -760,6 +770,7 @@ def _check_offsets(offsets: torch.Tensor) -> int:
 def _expert_rows(f, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                  out: Optional[torch.Tensor], stream, forward: bool) -> torch.Tensor:
     """dmuon_expert_matmul and dmuon_expert_input_grad: rows in, rows out."""
+    _no_graph(name, a, w, out)
     experts, n, k, ldw, far = _rows3(w, "w")
     tokens, cols, lda = _rows2(a, "x" if forward else "dy")
     if cols != (k if forward else n):
@@ -787,7 +798,12 @@ def dmuon_expert_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = w[e] @ x[t] for the rows t of expert e, offsets[e] .. offsets[e + 1] - 1
     (x tokens x k, w experts x n x k, offsets int32 on the device).  Rows of no
-    expert are left as they were in ``out``, and are zero in an allocated result."""
+    expert are left as they were in ``out``, and are zero in an allocated result.
+
+    This call and the five below record no autograd graph and refuse tensors
+    that require a gradient where one would be recorded: call them under
+    torch.no_grad(), or in a torch.autograd.Function whose backward calls
+    dmuon_expert_input_grad and dmuon_expert_weight_grad."""
     return _expert_rows(_lib.dmuon_expert_matmul, "dmuon_expert_matmul", x, w, offsets, out, stream, True)
 
 
@@ -803,6 +819,7 @@ def dmuon_expert_weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.T
     """dw[e] = dy[rows of e].T @ x[rows of e]: the gradient of dmuon_expert_matmul's
     weights (experts x n x k, in x's dtype or float32), added to ``out`` with
     ``accumulate``.  Each dw[e] is a gradient for dmuon_step."""
+    _no_graph("dmuon_expert_weight_grad", dy, x, out)
     experts = _check_offsets(offsets)
     tokens, n, ld_n = _rows2(dy, "dy")
     rows, k, ld_k = _rows2(x, "x")
@@ -856,6 +873,7 @@ def dmuon_quantize_blocks(x: torch.Tensor, *, block_rows: int = 1, fmt: str = "e
     8-bit floating point with one fp32 scale per block_rows x 128 values, and,
     with ``transposed`` (or given qt and scale_t), the quantised transpose; qt
     and scale_t are None otherwise."""
+    _no_graph("dmuon_quantize_blocks", x, q, scale, qt, scale_t)
     dt = _FORMATS[fmt]
     d = _blocks_desc(x, dt, block_rows)
     device = _gpu(x)
@@ -882,6 +900,7 @@ def dmuon_dequantize_blocks(q: torch.Tensor, scale: torch.Tensor, *, block_rows:
                             dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                             stream=None) -> torch.Tensor:
     """The values that (q, scale) of dmuon_quantize_blocks stand for."""
+    _no_graph("dmuon_dequantize_blocks", q, scale, out)
     device = _gpu(q)
     x = out if out is not None else _result(device, stream, q.shape, dtype)
     if x.shape != q.shape:
@@ -904,6 +923,7 @@ def dmuon_block_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, 
     1 x 128 blocks, b n x k with block_rows x 128 blocks), in bfloat16 or
     float32, added to ``out`` with ``accumulate``.  With ``offsets`` b holds
     one matrix per expert (experts x n x k), as in dmuon_expert_matmul."""
+    _no_graph("dmuon_block_matmul", a, a_scale, b, b_scale, out)
     m, k, lda = _rows2(a, "a")
     if offsets is not None:
         experts, n, kb, ldb, far = _rows3(b, "b")

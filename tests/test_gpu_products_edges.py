@@ -24,3 +24,36 @@ def test_stream_handle_without_the_raw_getter(lib, monkeypatch):
         y = lib.dmuon_expert_matmul(x, w, offs)
     side.synchronize()
     assert bool((y == 16).all())
+
+
+class _Experts(torch.autograd.Function):
+    """The three products joined as their documentation says."""
+
+    @staticmethod
+    def forward(ctx, lib, x, w, offs):
+        ctx.lib = lib
+        ctx.save_for_backward(x, w, offs)
+        return lib.dmuon_expert_matmul(x, w, offs)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offs = ctx.saved_tensors
+        dy = dy.contiguous()
+        return None, ctx.lib.dmuon_expert_input_grad(dy, w, offs), ctx.lib.dmuon_expert_weight_grad(dy, x, offs), None
+
+
+def test_products_inside_an_autograd_function(lib):
+    """The gradients that autograd hands on are the gradient products'; the
+    bare call refuses the same tensors."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(30, 24, generator=g, device=DEV).requires_grad_()
+    w = torch.randn(2, 16, 24, generator=g, device=DEV).requires_grad_()
+    offs = torch.tensor([0, 11, 30], dtype=torch.int32, device=DEV)
+    y = _Experts.apply(lib, x, w, offs)
+    dy = torch.randn(30, 16, generator=g, device=DEV)
+    y.backward(dy)
+    with torch.no_grad():
+        assert torch.equal(x.grad, lib.dmuon_expert_input_grad(dy, w, offs))
+        assert torch.equal(w.grad, lib.dmuon_expert_weight_grad(dy, x, offs))
+    with pytest.raises(ValueError, match="gradient"):
+        lib.dmuon_expert_matmul(x, w, offs)
