@@ -731,14 +731,15 @@ def _result(device, stream, shape, dtype, zero=False) -> torch.Tensor:
 
 
 def _rows2(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
-    """(rows, columns, row stride) of a 2-D tensor whose rows are contiguous."""
+    """(rows, columns, row stride) of a 2-D tensor whose rows are contiguous; the
+    stride of a single row, which no access uses, counts as its length."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return rows, cols, ld if rows > 1 else cols if ld < cols else ld
+    return rows, cols, ld if rows > 1 else cols
 
 
 def _rows3(t: torch.Tensor, name: str) -> Tuple[int, int, int, int, int]:

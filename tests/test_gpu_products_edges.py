@@ -57,3 +57,26 @@ def test_products_inside_an_autograd_function(lib):
         assert torch.equal(w.grad, lib.dmuon_expert_weight_grad(dy, x, offs))
     with pytest.raises(ValueError, match="gradient"):
         lib.dmuon_expert_matmul(x, w, offs)
+
+
+def test_one_row_of_a_long_prompt(lib):
+    """hidden[:, -1] of one sequence: a row with a stride above 2^22."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k, n = 1024, 64
+    x = torch.randn(1, 4200, k, generator=g, device=DEV).to(BF)[:, -1]
+    assert x.stride(0) > 1 << 22 and x.data_ptr() % 16 == 0
+    w = torch.randn(1, n, k, generator=g, device=DEV).to(BF)
+    dy = torch.randn(1, 70000, n, generator=g, device=DEV).to(BF)[:, -1]
+    offs = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    flat, dflat = x.clone(), dy.clone()
+    assert torch.equal(lib.dmuon_expert_matmul(x, w, offs), lib.dmuon_expert_matmul(flat, w, offs))
+    assert torch.equal(lib.dmuon_expert_input_grad(dy, w, offs), lib.dmuon_expert_input_grad(dflat, w, offs))
+    assert torch.equal(lib.dmuon_expert_weight_grad(dy, x, offs), lib.dmuon_expert_weight_grad(dflat, flat, offs))
+    q, s, qt, st = lib.dmuon_quantize_blocks(x, transposed=True)
+    want = lib.dmuon_quantize_blocks(flat, transposed=True)
+    assert all(torch.equal(a.float(), b.float()) for a, b in zip((q, s, qt, st), want))
+    out = torch.zeros(1, 70000, n, dtype=BF, device=DEV)
+    wq, ws, _, _ = lib.dmuon_quantize_blocks(w[0], block_rows=128)
+    y = lib.dmuon_block_matmul(q, s, wq, ws, out=out[:, -1])
+    assert torch.equal(y, lib.dmuon_block_matmul(q, s, wq, ws))
+    assert not bool(out[:, :-1].any())

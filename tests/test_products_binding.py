@@ -61,3 +61,13 @@ def test_no_gradient_is_lost_in_silence(call):
         f(wants)
     with pytest.raises(ValueError, match="GPU"):
         f(lambda t: t)
+
+
+def test_one_row_of_any_stride():
+    """The last token of a long prompt is one row with the prompt's stride,
+    which no access uses: rows of 2^22 elements and more apart are taken."""
+    import matrix_optimizer_step_owned_amd as dm
+    far = torch.empty_strided((1, 64), (1 << 24, 1), dtype=torch.bfloat16)
+    assert dm._rows2(far, "x") == (1, 64, 64)
+    assert dm._rows2(far[:0], "x") == (0, 64, 64)
+    assert dm._rows2(torch.empty(5, 80)[:, :64], "x") == (5, 64, 80)
