@@ -902,18 +902,23 @@ int64_t skinny_blocks(const BlockArgs& P, int mb, int nb) {
   const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
   return (P.m / (16 * mb) + used) * ((P.n + 16 * nb - 1) / (16 * nb));
 }
-template <int MB, int NB>
-hipError_t launch_skinny(const BlockArgs& P, int a5, int b5, int b_rows, bool f32, hipStream_t stream) {
+template <int MB, int NB, typename OutT>
+hipError_t launch_skinny(const BlockArgs& P, int a5, int b5, int b_rows, hipStream_t stream) {
   const int64_t blocks = skinny_blocks(P, MB, NB);
   const dim3 grid(static_cast<unsigned>(blocks));
-  if (skinny_waves(blocks) == 8) {
-    if (f32) hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 8, float>), grid, dim3(512), 0, stream, P, a5, b5, b_rows);
-    else hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 8, uint16_t>), grid, dim3(512), 0, stream, P, a5, b5, b_rows);
-  } else {
-    if (f32) hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 16, float>), grid, dim3(1024), 0, stream, P, a5, b5, b_rows);
-    else hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 16, uint16_t>), grid, dim3(1024), 0, stream, P, a5, b5, b_rows);
+  if constexpr (skinny_sixteen(MB, NB, sizeof(OutT) == 4)) {
+    if (blocks < kSkinnyWide) {
+      hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 16, OutT>), grid, dim3(1024), 0, stream, P, a5, b5, b_rows);
+      return hipGetLastError();
+    }
   }
+  hipLaunchKernelGGL((block_skinny_kernel<MB, NB, 8, OutT>), grid, dim3(512), 0, stream, P, a5, b5, b_rows);
   return hipGetLastError();
+}
+template <int MB, int NB>
+hipError_t launch_skinny(const BlockArgs& P, int a5, int b5, int b_rows, bool f32, hipStream_t stream) {
+  return f32 ? launch_skinny<MB, NB, float>(P, a5, b5, b_rows, stream)
+             : launch_skinny<MB, NB, uint16_t>(P, a5, b5, b_rows, stream);
 }
 
 template <bool A5, bool B5, bool BROWS, typename OutT>

@@ -372,10 +372,13 @@ template <int MB, int NB>
 hipError_t launch_skinny(const ExpertArgs& P, hipStream_t stream) {
   const int64_t blocks = skinny_blocks(P, MB, NB);
   const dim3 grid(static_cast<unsigned>(blocks));
-  if (skinny_waves(blocks) == 8)
-    hipLaunchKernelGGL((expert_skinny_kernel<MB, NB, 8>), grid, dim3(512), 0, stream, P);
-  else
-    hipLaunchKernelGGL((expert_skinny_kernel<MB, NB, 16>), grid, dim3(1024), 0, stream, P);
+  if constexpr (skinny_sixteen(MB, NB, false)) {
+    if (blocks < kSkinnyWide) {
+      hipLaunchKernelGGL((expert_skinny_kernel<MB, NB, 16>), grid, dim3(1024), 0, stream, P);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((expert_skinny_kernel<MB, NB, 8>), grid, dim3(512), 0, stream, P);
   return hipGetLastError();
 }
 

@@ -101,8 +101,13 @@ constexpr int64_t kMaxSkinnyBlocks = int64_t(1) << 23;
 // but take the same load path as the weights; worth it while enough blocks remain.
 constexpr int64_t kSkinnyWide = 256;
 
-// Waves per block (measured: 7 x 14336 x 4096 in 8 bits, 448 blocks: 15.2 us with
-// eight waves, 15.7 with four; 64 blocks of 16 waves 6.3 us).
-inline int skinny_waves(int64_t blocks) { return blocks >= 256 ? 8 : 16; }
+// Waves per block: eight (7 x 14336 x 4096 in 8 bits, 448 blocks: 15.2 us, 15.7
+// with four), and sixteen for fewer blocks than CUs of the smallest form (4 rows
+// of 1024 x 14336, weights from HBM: bf16 22.2 us against 23.1 with eight, 8-bit
+// 14.5 against 15.8).  Sixteen waves leave a lane 128 registers, which the larger
+// forms and those with fp32 results exceed: they then keep up to 215 in scratch
+// memory (17 rows of 4096 x 4096, sixteen and eight waves: bf16 35.5 and 17.3 us,
+// 8-bit 34.2 and 11.2, with fp32 results 34.0 and 12.9).
+constexpr bool skinny_sixteen(int mb, int nb, bool f32) { return mb * nb == 1 && !f32; }
 
 }  // namespace dmuon
