@@ -716,11 +716,10 @@ def _gpu(t: torch.Tensor):
 def _no_graph(name: str, *tensors) -> None:
     """Refuses a call that autograd would have to record: the library records
     no graph, so the result's gradient would be lost in silence."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{name} records no graph, and a tensor requires a gradient: call it under "
-                                 "torch.no_grad() or on detached tensors")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} records no graph, and a tensor requires a gradient: call it under "
+                             "torch.no_grad() or on detached tensors")
 
 
 def _result(device, stream, shape, dtype, zero=False) -> torch.Tensor:
