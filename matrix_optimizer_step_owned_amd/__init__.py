@@ -867,13 +867,17 @@ def _dense(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
 
 
 def dmuon_quantize_blocks(x: torch.Tensor, *, block_rows: int = 1, fmt: str = "e4m3", transposed: bool = False,
-                          q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                          plain: bool = True, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
                           qt: Optional[torch.Tensor] = None, scale_t: Optional[torch.Tensor] = None, stream=None):
     """(q, scale, qt, scale_t): x (rows x cols, or a batch of matrices) in
     8-bit floating point with one fp32 scale per block_rows x 128 values, and,
     with ``transposed`` (or given qt and scale_t), the quantised transpose; qt
-    and scale_t are None otherwise."""
+    and scale_t are None otherwise.  Without ``plain`` the transpose alone is
+    written, and q and scale are None."""
     _no_graph("dmuon_quantize_blocks", x, q, scale, qt, scale_t)
+    transposed = transposed or qt is not None or scale_t is not None
+    if not plain and (not transposed or q is not None or scale is not None):
+        raise ValueError("without plain the transpose has to be asked for, and no q or scale given")
     dt = _FORMATS[fmt]
     d = _blocks_desc(x, dt, block_rows)
     device = _gpu(x)
@@ -885,14 +889,15 @@ def dmuon_quantize_blocks(x: torch.Tensor, *, block_rows: int = 1, fmt: str = "e
         s = _dense(s, names[1], ss, torch.float32) if s is not None else _result(device, stream, ss, torch.float32)
         return q, s
 
-    q, scale = pair(q, scale, d.rows, d.cols, ("q", "scale"))
-    if transposed or qt is not None or scale_t is not None:
+    if plain:
+        q, scale = pair(q, scale, d.rows, d.cols, ("q", "scale"))
+    if transposed:
         qt, scale_t = pair(qt, scale_t, d.cols, d.rows, ("qt", "scale_t"))
     _same_device(device, q, scale, qt, scale_t)
     if x.numel():
-        _launch(_lib.dmuon_quantize_blocks, "dmuon_quantize_blocks", device, stream, d, x.data_ptr(), q.data_ptr(),
-                scale.data_ptr(), qt.data_ptr() if qt is not None else None,
-                scale_t.data_ptr() if scale_t is not None else None)
+        _launch(_lib.dmuon_quantize_blocks, "dmuon_quantize_blocks", device, stream, d, x.data_ptr(),
+                q.data_ptr() if q is not None else None, scale.data_ptr() if scale is not None else None,
+                qt.data_ptr() if qt is not None else None, scale_t.data_ptr() if scale_t is not None else None)
     return q, scale, qt, scale_t
 
 

@@ -80,3 +80,19 @@ def test_one_row_of_a_long_prompt(lib):
     y = lib.dmuon_block_matmul(q, s, wq, ws, out=out[:, -1])
     assert torch.equal(y, lib.dmuon_block_matmul(q, s, wq, ws))
     assert not bool(out[:, :-1].any())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_transpose_alone(lib, block_rows, dtype):
+    """The quantised transpose without the plain copy is the pair's."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    for shape in ((1, 1), (130, 257), (3, 64, 384)):
+        x = torch.randn(shape, generator=g, device=DEV).to(dtype)
+        _, _, qt, st = lib.dmuon_quantize_blocks(x, block_rows=block_rows, transposed=True)
+        none, none_s, got, scale = lib.dmuon_quantize_blocks(x, block_rows=block_rows, transposed=True, plain=False)
+        assert none is None and none_s is None
+        assert torch.equal(got.float(), qt.float()) and torch.equal(scale, st)
+        got.view(torch.uint8).zero_()
+        lib.dmuon_quantize_blocks(x, block_rows=block_rows, plain=False, qt=got, scale_t=scale)
+        assert torch.equal(got.float(), qt.float())

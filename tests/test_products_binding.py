@@ -71,3 +71,11 @@ def test_one_row_of_any_stride():
     assert dm._rows2(far, "x") == (1, 64, 64)
     assert dm._rows2(far[:0], "x") == (0, 64, 64)
     assert dm._rows2(torch.empty(5, 80)[:, :64], "x") == (5, 64, 80)
+
+
+def test_transpose_alone_refusals():
+    import matrix_optimizer_step_owned_amd as dm
+    x, q, s = torch.zeros(4, 8), torch.zeros(4, 8, dtype=torch.float8_e4m3fn), torch.zeros(4, 1)
+    for kw in (dict(), dict(transposed=True, q=q), dict(transposed=True, scale=s)):
+        with pytest.raises(ValueError, match="plain"):
+            dm.dmuon_quantize_blocks(x, plain=False, **kw)
