@@ -215,3 +215,42 @@ def test_block_product(lib, case, fmts, br):
             err = (got[lo:hi].double() - ref).abs()
             assert bool((err <= tol).all()), (e, float((err / tol).max()))
             within(wide[lo:hi], ref, A.abs() @ B.abs().t().contiguous(), k + 3 * -(-k // 128) + 1, F32, ("fp32", e))
+
+
+@pytest.mark.parametrize("fmts", ["e4m3-e4m3", "e5m2-e4m3", "e4m3-e5m2", "e5m2-e5m2"])
+@pytest.mark.parametrize("m,n", [(7, 64), (40, 72), (300, 130), (2000, 2100), (768, 16400)])
+def test_sums_that_cancel(lib, m, n, fmts):
+    """Each row of a holds pairs of opposite values against equal ones of b, the
+    largest of the format among them, and a small remainder: the results are far
+    smaller than the products.  Few-rows, 64-, 128- and 256-tiles."""
+    fa, fb = fmts.split("-")
+    gen = torch.Generator(device=DEV).manual_seed(m)
+    k = 256
+    av, bv = torch.randn(m, k, generator=gen, device=DEV) * 20, torch.randn(n, k, generator=gen, device=DEV) * 20
+    for c in (0, 128):
+        av[:, c], bv[:, c] = 448.0, 448.0          # an outlier column
+        av[:, c + 60:c + 120], bv[:, c + 60:c + 120] = -av[:, c:c + 60], bv[:, c:c + 60]
+    a, b = av.clamp(-448, 448).to(Q8[fa][0]), bv.clamp(-448, 448).to(Q8[fb][0])
+    sa = torch.full((m, 2), 2.0 ** -5, device=DEV)
+    sb = torch.full((n, 2), 2.0 ** -7, device=DEV)
+    got = lib.dmuon_block_matmul(a, sa, b, sb, block_rows=1)
+    A, pa = values(a, sa, 1, fa)
+    B, pb = values(b, sb, 1, fb)
+    ref, tol = block_bound(A, pa, B, pb)
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    wide = lib.dmuon_block_matmul(a, sa, b, sb, block_rows=1, out_dtype=F32)
+    within(wide, ref, A.abs() @ B.abs().t().contiguous(), k + 9, F32, "fp32")
+
+
+def test_what_the_instruction_keeps(lib):
+    """Beside two products of 2^15 that cancel, a product of 2^2 (2^-13 of them) in
+    the same eight is kept; in another eight one of 2^-7 is."""
+    a = torch.zeros(4, 128, device=DEV)
+    a[:, 0], a[:, 1] = 2.0 ** 15, -2.0 ** 15
+    a[0, 2], a[1, 7], a[2, 8], a[3, 100] = 4.0, -4.0, 2.0 ** -7, -2.0 ** -7
+    b = torch.ones(16, 128, device=DEV).to(torch.float8_e4m3fn)
+    one = torch.ones(4, 1, device=DEV)
+    c = lib.dmuon_block_matmul(a.to(torch.float8_e5m2), one, b, torch.ones(16, 1, device=DEV), block_rows=1)
+    want = torch.tensor([4.0, -4.0, 2.0 ** -7, -2.0 ** -7], device=DEV).to(BF)
+    assert torch.equal(c, want[:, None].expand(4, 16))
