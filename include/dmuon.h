@@ -437,7 +437,8 @@ int dmuon_assign_owners(const int64_t* rows, const int64_t* cols, int32_t n, int
  * shorter than a row or an expert, a misaligned or NULL buffer, accumulate
  * other than 0 or 1 or with another call than the weight gradient;
  * UNSUPPORTED for other dtypes or more than 2^24 - 4096 tiles of 128 x 128;
- * ALIASING when the result overlaps an operand.
+ * ALIASING when the memory from the result's first element to its last meets
+ * an operand's (gaps between rows count: two column ranges of one buffer meet).
  */
 typedef struct {
   int64_t tokens;          /* rows of x, y, dx, dy                              */
@@ -471,7 +472,8 @@ int dmuon_expert_weight_grad(const dmuon_experts_t* d, const void* dy, const voi
  * rows, its blocks along the rows of x): what a product that sums over the
  * rows of x reads.  Either pair may be NULL.  A block that holds a NaN or an
  * Inf gets a non-finite scale and decodes to NaN; other blocks are not
- * affected.  dmuon_dequantize_blocks writes x = q * scale, rounded once.
+ * affected.  dmuon_dequantize_blocks writes x = q * scale in fp32, for BF16
+ * then rounded to nearest even.
  * x is batch matrices of rows x cols with row stride ldx, x_stride elements
  * apart.  rows == 0 does nothing.  Errors as above (rows 0..2^30, cols and
  * ldx 1..2^22, batch 1..65535, at most 2^24 - 4096 pieces of 16 x 128).

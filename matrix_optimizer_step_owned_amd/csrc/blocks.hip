@@ -252,7 +252,9 @@ __device__ __forceinline__ float from_q8(uint32_t b) {
   else return __builtin_amdgcn_cvt_f32_fp8(int(b), 0);
 }
 
-// q * scale in fp32, rounded once; one block per 128 columns x 16 rows.
+// q * scale in fp32, and for bf16 that rounded again, as plain fp32 code has it (at
+// most 2^-24 of a value more than half a bf16 step); one block per 128 columns x
+// 16 rows.
 template <bool F32, bool E5M2>
 __global__ void __launch_bounds__(256)
 dequantize_kernel(QuantArgs P) {
@@ -979,7 +981,10 @@ hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, boo
   const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
   const int64_t big = (P.m / kBig + used) * ((P.n + kBig - 1) / kBig);
   // 256-tiles from 192 on (2048 x 4096 x 4096, 128 of them: 62 us so, 57 in
-  // 128-tiles); offsets of a tile's rows within 31 bits
+  // 128-tiles); offsets of a tile's rows within 31 bits.  With few rows per expert
+  // too: both kernels then only read the weights (one row per expert, from HBM,
+  // these tiles and the few-rows kernel: 8 experts of 14336 x 4096 128 and 118 us,
+  // 16 of 4096 x 4096 73 and 71, 64 of 2048 x 2048 67 and 84, 32 of 4096 x 512 22 and 58)
   const bool fits = P.lda <= kMaxBigPitch && P.ldb <= kMaxBigPitch && P.experts <= kBigExperts;
   if (vec && !f32 && fits && big >= 192) {
     const unsigned blocks = static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks);

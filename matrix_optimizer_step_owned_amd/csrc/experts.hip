@@ -316,9 +316,11 @@ struct ExpertBig {
   }
 };
 
-// 8192^3: 1.40 to 1.43 PFLOP/s in all three directions, the board at its power
-// cap.  8 experts of 14336 x 4096, 8192 even rows: forward 885 us, input gradient
-// 770 (long sums), weight gradient 880 (short sums).
+// 8192^3: 1.40 to 1.45 PFLOP/s in all three directions, the board at its power
+// cap.  8 experts of 14336 x 4096, 8192 even rows: forward 903 us, input gradient
+// 756 (long sums), weight gradient 875 (short sums); uneven ones (deviation 0.5 of
+// the logarithm) 875, 857 and 887, from 823 for the forward in another run: the
+// clock under the cap decides the last 5 %.
 template <int OP, typename OutT>
 __global__ void __launch_bounds__(kBigThreads)
 expert_bf16_big_kernel(ExpertArgs P) {
@@ -530,7 +532,13 @@ int64_t tile_bound(const ExpertArgs& P, int64_t t) {
 template <int OP>
 hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hipStream_t stream) {
   // 256-tiles from half a tile per CU on: 8 experts of 2048 x 2048, 2048 rows,
-  // take 35 us so and 38 in 128-tiles, their weight gradient 30 and 46
+  // take 35 us so and 38 in 128-tiles, their weight gradient 30 and 46.  Experts
+  // with few rows come here too, down to one: both kernels then only read the
+  // weights, and neither is ahead everywhere (forward, one row per expert,
+  // weights from HBM, these tiles and the few-rows kernel: 8 experts of 14336 x 4096
+  // 165 and 177 us, 8 of 8192 x 8192 182 and 210, 32 of 4096 x 512 28 and 35, but 16
+  // of 4096 x 4096 125 and 105, 64 of 2048 x 2048 134 and 93); with eight rows and
+  // more the tiles stay as they are and the other grows by 3 to 20 %.
   const int64_t big = tile_bound<OP>(P, kBig);
   if (dtype == DT_BF16 && vec && big >= 128 && P.experts <= kBigExperts) {
     const dim3 grid(static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks)), block(kBigThreads);
@@ -546,8 +554,7 @@ hipError_t launch_op(const ExpertArgs& P, int dtype, int out_dtype, bool vec, hi
   if constexpr (OP == OP_FORWARD) {
     // too few tiles to fill the GPU and at most 16, or 32, rows per expert on
     // average: one 4096 x 4096 expert takes 54 us for 4 rows in 128-tiles,
-    // 5 us here; with 448 tiles (8 experts of 14336 x 4096) the tiles are
-    // faster from 2 rows per expert on
+    // 10 us here (weights from HBM)
     if (dtype == DT_BF16 && vec && skinny_blocks(P, 1, 1) <= kMaxSkinnyBlocks) {
       if (P.tokens <= 16 * int64_t(P.experts)) {
         if (skinny_blocks(P, 1, 2) >= kSkinnyWide) return launch_skinny<1, 2>(P, stream);
