@@ -2,8 +2,9 @@
 
 Builds a copy of the package whose host code is compiled with
 AddressSanitizer and UndefinedBehaviorSanitizer (device code as usual), then
-runs the host-only tests -- the ABI and planner tests and the owner planner's
-parity tests -- against that library with the ASan runtime preloaded into
+runs the host-only tests -- the ABI and planner tests, the owner planner's
+parity tests and the refusals of the expert products and 8-bit blocks --
+against that library with the ASan runtime preloaded into
 Python.  Any sanitizer report aborts the run with a non-zero exit status.
 
     python tests/sanitize_host.py [--keep DIR]
@@ -27,7 +28,7 @@ import _build  # noqa: E402  (the package's own source list and compile flags)
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer",
             "-Xarch_host", "-shared-libsan"]
-TESTS = ["tests/test_abi_host.py", "tests/test_owners.py"]
+TESTS = ["tests/test_abi_host.py", "tests/test_owners.py", "tests/test_products_host.py"]
 
 
 def asan_runtime() -> str:
