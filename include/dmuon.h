@@ -505,7 +505,8 @@ int dmuon_dequantize_blocks(const dmuon_blocks_t* d, const void* q, const float*
  * dmuon_expert_matmul.  experts == 0: one product, offsets NULL.
  * bf16 results come from the 8-bit matrix instructions, which cut every
  * product toward zero at 2^-13 of the largest of its eight neighbours along k
- * (k = 8 i .. 8 i + 7) before they add in fp32: results much smaller than their
+ * (k = 8 i .. 8 i + 7; a subnormal operand counts as the smallest normal number
+ * there) before they add in fp32: results much smaller than their
  * products can be off by more than bf16 rounding.  fp32 results come from
  * operands widened to bf16 (exactly), which keep fp32 sums at half the rate:
  * take them where large products cancel, or where many calls accumulate.

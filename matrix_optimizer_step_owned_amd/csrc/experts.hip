@@ -319,8 +319,8 @@ struct ExpertBig {
 // 8192^3: 1.40 to 1.45 PFLOP/s in all three directions, the board at its power
 // cap.  8 experts of 14336 x 4096, 8192 even rows: forward 903 us, input gradient
 // 756 (long sums), weight gradient 875 (short sums); uneven ones (deviation 0.5 of
-// the logarithm) 875, 857 and 887, from 823 for the forward in another run: the
-// clock under the cap decides the last 5 %.
+// the logarithm) 875, 857 and 887.  Runs differ by 5 % with the clock under the cap
+// (the uneven forward took 823 in another).
 template <int OP, typename OutT>
 __global__ void __launch_bounds__(kBigThreads)
 expert_bf16_big_kernel(ExpertArgs P) {
