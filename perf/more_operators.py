@@ -79,9 +79,9 @@ def draw(rng):
     while True:
         op = rng.choice(["adamw8", "rows", "int8", "int8", "layer"])
         if op == "adamw8":
-            c = dict(op=op, matrices=rng.choice([0, 1, 1, 3, 12]), rows=_size(rng, 1, 128256), cols=_width(rng, 1, 14336),
-                     vectors=rng.choice([0, 1, 6, 57]), dtype=rng.choice(["bf16", "bf16", "f32"]),
-                     grad=rng.choice(["bf16", "bf16", "f32"]), packed=rng.random() < 0.3)
+            c = dict(op=op, matrices=rng.choice([0, 1, 1, 3, 12]), rows=_size(rng, 1, 128256),
+                     cols=_width(rng, 1, 14336), vectors=rng.choice([0, 1, 6, 57]),
+                     dtype=rng.choice(["bf16", "bf16", "f32"]), grad=rng.choice(["bf16", "bf16", "f32"]), packed=rng.random() < 0.3)
             c["rows"] = c["rows"] if c["matrices"] else 0
             if 1 <= c["cols"] * (c["matrices"] * c["rows"] + c["vectors"]) <= MAX_STATES // 2:
                 return c
@@ -189,7 +189,9 @@ def _prepare_adamw8(case, gen):
     g[:n // 64 * 64].view(n // 64, 64).mul_(torch.exp(1.5 * _normal(gen, (n // 64, 1), 1.0)))
     root = g.abs().mul_(0.5 + torch.rand(n, generator=gen, device=DEV))
     avg = g * 0.3 + root * _normal(gen, (n,), 0.2)
-    s = dict(step=100, seed=int(torch.randint(2 ** 31, (1,), generator=gen, device=DEV)), p=_normal(gen, (n,), 0.02, DT[case["dtype"]]), g=(g + 1e-4 * _normal(gen, (n,), 1.0)).to(DT[case["grad"]]))
+    s = dict(step=100, seed=int(torch.randint(2 ** 31, (1,), generator=gen, device=DEV)))
+    s["p"] = _normal(gen, (n,), 0.02, DT[case["dtype"]])
+    s["g"] = (g + 1e-4 * _normal(gen, (n,), 1.0)).to(DT[case["grad"]])
     s["avg"] = torch.zeros(n, dtype=torch.float8_e4m3fn, device=DEV)
     s["root"] = torch.zeros(n, dtype=torch.float8_e4m3fn, device=DEV)
     s["avg_scale"] = torch.zeros(ns, device=DEV)
@@ -319,15 +321,15 @@ def _run_own(s):
     op = s["op"]
     if op == "adamw8":
         s["step"] += 1
-        dm.dmuon_adamw8_step(s["ps"], s["gs"], s["avgs"], s["avg_scales"], s["roots"], s["root_scales"],
-                             groups=[dict(h, step=s["step"]) for h in GROUPS], group_index=s["group_index"],
-                             seed=s["seed"])
+        dm.dmuon_adamw_step_quantized(s["ps"], s["gs"], s["avgs"], s["avg_scales"], s["roots"], s["root_scales"],
+                                      groups=[dict(h, step=s["step"]) for h in GROUPS], group_index=s["group_index"],
+                                      seed=s["seed"])
         return _states(s)
     if op == "rows":
         q, scale = dm.dmuon_quantize_rows(s["x"], activation="swiglu" if s["glu"] else None, q=s["q"], scale=s["scale"])
         return (dm.dmuon_dequantize_rows(q, scale, out=s["values"]) if s["glu"] else q), scale
     if op == "int8":
-        return dm.dmuon_int8_matmul(s["a"], s["a_scale"], s["b"], s["b_scale"], offsets=s["offsets"], out=s["c"])
+        return dm.dmuon_row_matmul(s["a"], s["a_scale"], s["b"], s["b_scale"], offsets=s["offsets"], out=s["c"])
     return dm.dmuon_expert_layer(s["x"], s["ids"], s["gates"], s["w_in"], s["w_out"], in_scale=s["in_scale"],
                                  out_scale=s["out_scale"], out=s["y"])
 
