@@ -70,7 +70,9 @@ typedef enum {
   DMUON_BF16 = 1,
   /* 8-bit floating point (OCP), of quantised blocks only */
   DMUON_E4M3 = 2,
-  DMUON_E5M2 = 3
+  DMUON_E5M2 = 3,
+  /* 8-bit integers, of quantised rows only */
+  DMUON_I8 = 4
 } dmuon_dtype_t;
 
 /* Training Guide, Hyperparameter Guide table, ns_backend row. */
@@ -527,6 +529,137 @@ typedef struct {
 
 int dmuon_block_matmul(const dmuon_block_product_t* d, const void* a, const float* a_scale, const void* b,
                        const float* b_scale, const int32_t* offsets, void* c, void* stream);
+
+/*
+ * AdamW with both states in 8 bits (dmuon_adamw_step holds them in fp32):
+ *   m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr wd) - (lr / (1 - beta1^t)) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * exp_avg holds m and root holds sqrt(v), each as E4M3 values with one fp32
+ * scale per 128 consecutive elements (the last block may be shorter): the
+ * 1 x 128 blocks that dmuon_quantize_blocks writes and dmuon_dequantize_blocks
+ * reads of the tensor's elements in rows of 128.  States start as zeros, scales too.
+ * In between everything is fp32.  New scales are max(amax / 448, 2^-126); with
+ * y = x * (1 / scale), m is rounded to nearest even, and r = sqrt(v), which a
+ * step moves by less than its neighbours are apart, at random:
+ *   r's steps of E4M3 at y = floor(y / spacing + u / 2^16)
+ * where u is the low (even i) or high (odd i) half of
+ *   H(H(key + i / 8192) + (i / 2) % 4096),  key = H(H(H(seed) + t) + place),
+ * i the element, t the group's step, place the tensor's index in the call and H
+ * the 32-bit finaliser of MurmurHash3 of its argument + 0x9e3779b9 (all modulo
+ * 2^32).  The same call on the same state gives the same bits; another step or
+ * seed other random numbers.  Every fp32 operation up to r is rounded by itself.
+ * A NaN or Inf in a gradient makes the states of its block of 128 NaN;
+ * parameters of its neighbours follow from the next step on.
+ * Tensors without a gradient (NULL) or elements are left as they are.  Any
+ * numel 0..2^42, buffers aligned to their elements.  No workspace: the tables
+ * travel as kernel arguments (40 tensors and 16 groups per launch).  A captured
+ * call repeats its step number on replay.
+ * Errors as for dmuon_adamw_step; no two buffers may overlap.
+ */
+typedef struct {
+  int64_t numel;
+  void* param;             /* device, in place                                 */
+  const void* grad;        /* device, or NULL: skip this tensor                */
+  void* exp_avg;           /* device, numel E4M3 values, in place              */
+  float* exp_avg_scale;    /* device, ceil(numel / 128), in place              */
+  void* root;              /* device, numel E4M3 values, in place              */
+  float* root_scale;       /* device, ceil(numel / 128), in place              */
+  int32_t param_dtype;     /* DMUON_F32 or DMUON_BF16                          */
+  int32_t grad_dtype;
+  int32_t group;           /* index into groups                                */
+  int32_t pad_;
+} dmuon_adamw_quantized_t;
+
+int dmuon_adamw_step_quantized(const dmuon_adamw_quantized_t* tensors, int32_t n, const dmuon_adamw_group_t* groups,
+                      int32_t ngroups, uint32_t seed, void* stream);
+
+/*
+ * 8-bit integers with one fp32 scale per row: a token of activations, or an
+ * output channel of a weight (n x k with its channels as rows).
+ * dmuon_quantize_rows writes
+ *   scale = max(amax / 127, 2^-126),  q = x * (1 / scale), rounded to nearest even
+ * of every row in fp32.  With DMUON_ACT_SWIGLU a row of x is 2 cols long, gate then
+ * up, and silu(gate) * up, in fp32, is what is quantised.  A row that holds a
+ * NaN or an Inf gets a scale that is not finite and decodes to NaN; other rows
+ * are not affected.  dmuon_dequantize_rows writes x = q * scale in fp32, for BF16
+ * then rounded.  q is dense (rows x cols), scale has rows values, x rows are ldx
+ * apart.  rows == 0 does nothing.  Errors as for the block operators (cols
+ * 1..2^22, ldx up to 2^23).
+ */
+#define DMUON_ACT_NONE   0
+#define DMUON_ACT_SWIGLU 1
+typedef struct {
+  int64_t rows, cols;      /* of q                                             */
+  int64_t ldx;             /* row stride of x, elements                        */
+  int32_t x_dtype;         /* DMUON_F32 or DMUON_BF16                          */
+  int32_t activation;      /* quantise: DMUON_ACT_NONE or DMUON_ACT_SWIGLU     */
+} dmuon_rows_t;
+
+int dmuon_quantize_rows(const dmuon_rows_t* d, const void* x, void* q, float* scale, void* stream);
+int dmuon_dequantize_rows(const dmuon_rows_t* d, const void* q, const float* scale, void* x, void* stream);
+
+/*
+ * Matrix product of 8-bit integers with a scale per row of either operand:
+ *   c[i][j] = a_scale[i] b_scale[j] sum_k a[i][k] b[j][k]
+ * (added to c with accumulate).  a is m x k (tokens), b n x k (weights).  The sum
+ * is an exact int32, which k <= 131071 keeps from overflowing for any operands; it is
+ * converted to fp32, scaled by a_scale, then by b_scale, and rounded to out_dtype
+ * (after c was added).
+ * With experts > 0, rows offsets[e] .. offsets[e + 1] - 1 of a and c use expert
+ * e's b (experts x n x k, b_stride apart) and b_scale (experts x n); offsets as
+ * for dmuon_expert_matmul, rows of nobody are left as they were.  Rows may have
+ * any stride; operands that are 16-byte aligned and multiples of 16 long take wider
+ * accesses and the larger tiles.  m == 0 does nothing.  Errors as for dmuon_block_matmul.
+ */
+typedef struct {
+  int64_t m, n, k;
+  int64_t lda, ldb, ldc;   /* row strides, elements                            */
+  int64_t b_stride;        /* from expert to expert (unused below 2 experts)   */
+  int32_t experts;         /* 0: one product                                   */
+  int32_t out_dtype;       /* DMUON_F32 or DMUON_BF16                          */
+  int32_t accumulate;      /* 1 adds to c                                      */
+  int32_t pad_;
+} dmuon_row_product_t;
+
+int dmuon_row_matmul(const dmuon_row_product_t* d, const void* a, const float* a_scale, const void* b,
+                      const float* b_scale, const int32_t* offsets, void* c, void* stream);
+
+/*
+ * A whole layer of experts for at most 64 tokens (serving), in two kernels:
+ *   y[t] = sum over picks j of  gates[t][j] w_out[e] (silu(G x[t]) * (U x[t])),  e = ids[t][j]
+ * with G the first n and U the last n rows of w_in[e].  x and y are tokens x k in
+ * bf16, ids and gates dense tokens x top_k, w_in experts x 2n x k, w_out experts x
+ * k x n, in bf16 or as 8-bit integers with a scale per row (in_scale experts x 2n,
+ * out_scale experts x k: what dmuon_quantize_rows makes of the weights' rows).
+ * ids are device data that the host never reads.  An id outside 0..experts - 1 is
+ * nobody's: that pick adds nothing, and a token without picks gets zeros.  A
+ * token may pick an expert twice: its gates add up.  Sums are fp32; the hidden
+ * activation times its gate is rounded to bf16, y is rounded once.  Results are
+ * deterministic.  A value that is not finite reaches its own token only, one of a
+ * weight only the tokens of its expert.
+ * workspace: dmuon_expert_layer_workspace_size bytes of device memory, 16-byte
+ * aligned, used while the call's kernels run.  tokens == 0 does nothing.  Calls may
+ * be captured into a HIP graph.
+ * Errors: INVALID_ARG for sizes outside the limits (tokens 0..64, top_k 1..64,
+ * experts 1..4096, n, k and row strides 1..2^22), strides shorter than a row or an
+ * expert, scales without 8-bit weights or the other way round, a misaligned or
+ * NULL buffer; UNSUPPORTED for other dtypes or more than 2^22 pieces of 16 columns
+ * of the picked experts' hidden activations; WORKSPACE; ALIASING.
+ */
+typedef struct {
+  int64_t tokens, n, k;    /* n: hidden features, k: features of x and y       */
+  int64_t ldx, ldy;        /* row strides, elements                            */
+  int64_t ld_in, ld_out;   /* row strides of w_in and w_out                    */
+  int64_t in_stride, out_stride;   /* from expert to expert (unused for one)   */
+  int32_t experts, top_k;
+  int32_t weight_dtype;    /* DMUON_BF16 or DMUON_I8                           */
+  int32_t pad_;
+} dmuon_expert_layer_t;
+
+size_t dmuon_expert_layer_workspace_size(const dmuon_expert_layer_t* d);
+int dmuon_expert_layer(const dmuon_expert_layer_t* d, const void* x, const int32_t* ids, const float* gates,
+                       const void* w_in, const float* in_scale, const void* w_out, const float* out_scale,
+                       void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Readable name of a status code (static storage). */
 const char* dmuon_status_string(int status);

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import json
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 import torch  # loaded first so that the library binds to torch's HIP runtime
@@ -35,6 +36,9 @@ DMUON_F32 = 0
 DMUON_BF16 = 1
 DMUON_E4M3 = 2
 DMUON_E5M2 = 3
+DMUON_I8 = 4
+DMUON_ACT_NONE = 0
+DMUON_ACT_SWIGLU = 1
 DMUON_NS_GRAM = 0
 DMUON_NS_DIRECT = 1
 DMUON_NS_PREC_BF16 = 0
@@ -109,6 +113,33 @@ class dmuon_block_product_t(ctypes.Structure):
                 ("accumulate", ctypes.c_int32)]
 
 
+class dmuon_adamw_quantized_t(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p), ("root", ctypes.c_void_p),
+                ("root_scale", ctypes.c_void_p), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
+class dmuon_rows_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class dmuon_row_product_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("experts", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
+class dmuon_expert_layer_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ld_in", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("in_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("pad_", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _I64P = ctypes.POINTER(ctypes.c_int64)
@@ -156,6 +187,14 @@ EXPORTS = {
     "dmuon_quantize_blocks": (ctypes.c_int, [ctypes.POINTER(dmuon_blocks_t), _P, _P, _P, _P, _P, _P]),
     "dmuon_dequantize_blocks": (ctypes.c_int, [ctypes.POINTER(dmuon_blocks_t), _P, _P, _P, _P]),
     "dmuon_block_matmul": (ctypes.c_int, [ctypes.POINTER(dmuon_block_product_t), _P, _P, _P, _P, _P, _P, _P]),
+    "dmuon_adamw_step_quantized": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(dmuon_adamw_group_t),
+                                                  ctypes.c_int32, ctypes.c_uint32, _P]),
+    "dmuon_quantize_rows": (ctypes.c_int, [ctypes.POINTER(dmuon_rows_t), _P, _P, _P, _P]),
+    "dmuon_dequantize_rows": (ctypes.c_int, [ctypes.POINTER(dmuon_rows_t), _P, _P, _P, _P]),
+    "dmuon_row_matmul": (ctypes.c_int, [ctypes.POINTER(dmuon_row_product_t), _P, _P, _P, _P, _P, _P, _P]),
+    "dmuon_expert_layer_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(dmuon_expert_layer_t)]),
+    "dmuon_expert_layer": (ctypes.c_int, [ctypes.POINTER(dmuon_expert_layer_t), _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                          ctypes.c_size_t, _P]),
     "dmuon_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "dmuon_last_error": (ctypes.c_char_p, []),
     "dmuon_backend_info": (ctypes.c_char_p, []),
@@ -515,6 +554,79 @@ def dmuon_adamw_step(params: List[torch.Tensor], grads: List[Optional[torch.Tens
     ws, wsb = _workspace(dmuon_adamw_workspace_size(n), params[0].device, workspace, stream)
     _check(_lib.dmuon_adamw_step(ta, n, ga, len(groups), ws.data_ptr() if ws is not None else None, wsb,
                                  _stream(stream, params[0].device)), "dmuon_adamw_step")
+
+
+_STATE_BLOCK = 128
+_ADAMW8_TENSOR = struct.Struct("<7q4i")      # dmuon_adamw_quantized_t
+
+
+def dmuon_adamw_quantized_state(param: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(exp_avg, exp_avg_scale, root, root_scale) of a parameter before its first
+    dmuon_adamw_step_quantized: zeros."""
+    blocks = -(-param.numel() // _STATE_BLOCK)
+    q = lambda: torch.zeros(param.shape, dtype=torch.uint8, device=param.device).view(torch.float8_e4m3fn)
+    scale = lambda: torch.zeros(blocks, dtype=torch.float32, device=param.device)
+    return q(), scale(), q(), scale()
+
+
+def dmuon_adamw_step_quantized(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Tensor]],
+                      exp_avgs: Sequence[torch.Tensor], exp_avg_scales: Sequence[torch.Tensor],
+                      roots: Sequence[torch.Tensor], root_scales: Sequence[torch.Tensor], *, step: int = 0,
+                      lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                      groups: Optional[Sequence[dict]] = None, group_index: Optional[Sequence[int]] = None,
+                      seed: int = 0, stream=None) -> None:
+    """One AdamW step over every tensor (in place) with both states in 8 bits:
+    exp_avgs (the first moments) and roots (the roots of the second ones) as
+    float8_e4m3fn of the parameters' sizes, with a float32 scale per 128 elements
+    in exp_avg_scales and root_scales (dmuon_adamw_quantized_state makes them).  ``seed``
+    and the step decide how the roots round.  Hyperparameters as for
+    dmuon_adamw_step: one set from the keywords, or ``groups`` with
+    ``group_index`` naming each tensor's group."""
+    n = len(params)
+    if not (len(grads) == len(exp_avgs) == len(exp_avg_scales) == len(roots) == len(root_scales) == n):
+        raise ValueError("one gradient and one of each state per parameter")
+    if n == 0:
+        return
+    if groups is None:
+        groups = [dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, step=step)]
+        group_index = [0] * n
+    if group_index is None or len(group_index) != n:
+        raise ValueError("group_index must name one group per tensor")
+    if not 0 <= int(seed) < 1 << 32:
+        raise ValueError("seed must be in 0 .. 2^32 - 1")
+    ga = (dmuon_adamw_group_t * len(groups))()
+    for k, h in enumerate(groups):
+        b1, b2 = h.get("betas", (0.9, 0.999))
+        ga[k] = dmuon_adamw_group_t(float(h.get("lr", 1e-3)), float(b1), float(b2), float(h.get("eps", 1e-8)),
+                                    float(h.get("weight_decay", 0.01)), int(h["step"]))
+    device = _gpu(params[0])
+    f8, f32, table, pack = torch.float8_e4m3fn, torch.float32, [], _ADAMW8_TENSOR.pack
+    for i, (p, g, m, ms, r, rs) in enumerate(zip(params, grads, exp_avgs, exp_avg_scales, roots, root_scales)):
+        numel = p.numel()
+        if m.dtype != f8 or r.dtype != f8 or ms.dtype != f32 or rs.dtype != f32:
+            raise TypeError(f"tensors[{i}]: states must be float8_e4m3fn, their scales float32")
+        blocks = (numel + _STATE_BLOCK - 1) // _STATE_BLOCK
+        if m.numel() != numel or r.numel() != numel or ms.numel() != blocks or rs.numel() != blocks:
+            raise ValueError(f"tensors[{i}]: states must have the parameter's size, scales one value per 128 elements")
+        if not (p.is_contiguous() and m.is_contiguous() and ms.is_contiguous() and r.is_contiguous()
+                and rs.is_contiguous()):
+            raise ValueError(f"tensors[{i}] must be contiguous")
+        dt = _DTYPES.get(p.dtype)
+        gdt, gp = dt, 0
+        if g is not None:
+            if g.numel() != numel or not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be contiguous and of the parameter's size")
+            gdt, gp = _DTYPES.get(g.dtype), g.data_ptr()
+            if g.device != device:
+                raise ValueError(f"a tensor is on {g.device}, not {device}")
+        if dt is None or gdt is None:
+            raise TypeError(f"tensors[{i}]: unsupported dtype")
+        if p.device != device or m.device != device or ms.device != device or r.device != device or rs.device != device:
+            raise ValueError(f"tensors[{i}] must be on {device}")
+        table.append(pack(numel, p.data_ptr(), gp, m.data_ptr(), ms.data_ptr(), r.data_ptr(), rs.data_ptr(), dt, gdt,
+                          int(group_index[i]), 0))
+    _launch(_lib.dmuon_adamw_step_quantized, "dmuon_adamw_step_quantized", device, stream, b"".join(table), n, ga,
+            len(groups), int(seed))
 
 
 DMUON_COST_NUMEL = 0
@@ -959,6 +1071,156 @@ def dmuon_block_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, 
                               1 if accumulate else 0)
     _launch(_lib.dmuon_block_matmul, "dmuon_block_matmul", device, stream, d, a.data_ptr(), a_scale.data_ptr(),
             b.data_ptr(), b_scale.data_ptr(), offsets.data_ptr() if offsets is not None else None, out.data_ptr())
+    return out
+
+
+_ACTIVATIONS = {None: DMUON_ACT_NONE, "swiglu": DMUON_ACT_SWIGLU}
+
+
+def dmuon_quantize_rows(x: torch.Tensor, *, activation: Optional[str] = None, q: Optional[torch.Tensor] = None,
+                        scale: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(q, scale): the rows of x (the last dimension; any number of leading ones)
+    as 8-bit integers with one fp32 scale per row: tokens of activations, or the
+    output channels of weights.  With activation="swiglu" a row of x is gate then
+    up, and silu(gate) * up is quantised.  A 2-D x may have any row stride."""
+    _no_graph("dmuon_quantize_rows", x, q, scale)
+    act = _ACTIVATIONS[activation]
+    if x.dim() < 2:
+        raise ValueError("x must be at least 2-D")
+    lead, wide = x.shape[:-1], x.shape[-1]
+    if x.dim() > 2:
+        if not x.is_contiguous():
+            raise ValueError("x of more than two dimensions must be contiguous")
+        rows, ldx = x.numel() // max(wide, 1), wide
+    else:
+        rows, _, ldx = _rows2(x, "x")
+    if act and wide % 2:
+        raise ValueError("gate and up must have the same number of columns")
+    cols = wide // 2 if act else wide
+    device, dt = _gpu(x), _dtype(x)
+    q = _dense(q, "q", lead + (cols,), torch.int8) if q is not None else \
+        _result(device, stream, lead + (cols,), torch.int8)
+    scale = _dense(scale, "scale", lead, torch.float32) if scale is not None else \
+        _result(device, stream, lead, torch.float32)
+    _same_device(device, q, scale)
+    if rows:
+        _launch(_lib.dmuon_quantize_rows, "dmuon_quantize_rows", device, stream, dmuon_rows_t(rows, cols, ldx, dt, act),
+                x.data_ptr(), q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def dmuon_dequantize_rows(q: torch.Tensor, scale: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values that (q, scale) of dmuon_quantize_rows stand for."""
+    _no_graph("dmuon_dequantize_rows", q, scale, out)
+    if q.dim() < 2:
+        raise ValueError("q must be at least 2-D")
+    device = _gpu(q)
+    _dense(q, "q", q.shape, torch.int8)
+    _dense(scale, "scale", q.shape[:-1], torch.float32)
+    x = out if out is not None else _result(device, stream, q.shape, dtype)
+    if x.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if x.dim() > 2:
+        if not x.is_contiguous():
+            raise ValueError("out of more than two dimensions must be contiguous")
+        rows, ldx = scale.numel(), q.shape[-1]
+    else:
+        rows, _, ldx = _rows2(x, "out")
+    _same_device(device, scale, x)
+    if rows:
+        _launch(_lib.dmuon_dequantize_rows, "dmuon_dequantize_rows", device, stream,
+                dmuon_rows_t(rows, q.shape[-1], ldx, _dtype(x), DMUON_ACT_NONE), q.data_ptr(), scale.data_ptr(),
+                x.data_ptr())
+    return x
+
+
+def dmuon_row_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, *,
+                      offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      out_dtype: torch.dtype = torch.bfloat16, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """c = (a @ b.T) * a_scale[:, None] * b_scale of 8-bit integers (a m x k, b
+    n x k, as dmuon_quantize_rows makes them) with exact sums, in bfloat16 or
+    float32, added to ``out`` with ``accumulate``.  With ``offsets`` b holds one
+    matrix per expert (experts x n x k, b_scale experts x n), as in
+    dmuon_expert_matmul; rows of no expert are left as they were in ``out``, and
+    are zero in an allocated result."""
+    _no_graph("dmuon_row_matmul", a, a_scale, b, b_scale, out)
+    m, k, lda = _rows2(a, "a")
+    if offsets is not None:
+        experts, n, kb, ldb, far = _rows3(b, "b")
+        if _check_offsets(offsets) != experts:
+            raise ValueError(f"offsets must have {experts + 1} entries")
+        _dense(b_scale, "b_scale", (experts, n), torch.float32)
+    else:
+        n, kb, ldb = _rows2(b, "b")
+        experts, far = 0, 0
+        _dense(b_scale, "b_scale", (n,), torch.float32)
+    if kb != k:
+        raise ValueError("a and b must have the same number of columns")
+    if a.dtype != torch.int8 or b.dtype != torch.int8:
+        raise TypeError("a and b must be int8")
+    _dense(a_scale, "a_scale", (m,), torch.float32)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    device = _gpu(a)
+    if out is None:
+        out = _result(device, stream, (m, n), out_dtype, zero=offsets is not None)
+    rows, cols, ldc = _rows2(out, "out")
+    if rows != m or cols != n:
+        raise ValueError(f"out must be {m} x {n}")
+    _same_device(device, a_scale, b, b_scale, offsets, out)
+    d = dmuon_row_product_t(m, n, k, lda, ldb, ldc, far, experts, _dtype(out), 1 if accumulate else 0)
+    _launch(_lib.dmuon_row_matmul, "dmuon_row_matmul", device, stream, d, a.data_ptr(), a_scale.data_ptr(),
+            b.data_ptr(), b_scale.data_ptr(), offsets.data_ptr() if offsets is not None else None, out.data_ptr())
+    return out
+
+
+_WEIGHTS = {torch.bfloat16: DMUON_BF16, torch.int8: DMUON_I8}
+
+
+def dmuon_expert_layer(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, w_in: torch.Tensor,
+                       w_out: torch.Tensor, *, in_scale: Optional[torch.Tensor] = None,
+                       out_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j gates[t, j] * w_out[e] @ (silu(G @ x[t]) * (U @ x[t])), e =
+    ids[t, j]: a whole layer of experts for at most 64 tokens (bf16, tokens x k),
+    with G and U the halves of the rows of w_in[e] (experts x 2n x k, w_out
+    experts x k x n), in bf16, or as 8-bit integers with the scales of
+    dmuon_quantize_rows (in_scale experts x 2n, out_scale experts x k).  ids int32
+    and gates float32, tokens x top_k; an id outside the experts is no pick."""
+    _no_graph("dmuon_expert_layer", x, gates, w_in, w_out, in_scale, out_scale, out)
+    tokens, k, ldx = _rows2(x, "x")
+    experts, n2, cols, ld_in, in_far = _rows3(w_in, "w_in")
+    e2, rows, n, ld_out, out_far = _rows3(w_out, "w_out")
+    if cols != k or rows != k or n2 != 2 * n or e2 != experts:
+        raise ValueError(f"w_in must be experts x 2n x {k} and w_out experts x {k} x n")
+    if x.dtype != torch.bfloat16 or w_in.dtype not in _WEIGHTS or w_out.dtype != w_in.dtype:
+        raise TypeError("x must be bfloat16, w_in and w_out both bfloat16 or both int8")
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise ValueError("ids must be tokens x top_k")
+    _dense(ids, "ids", ids.shape, torch.int32)
+    _dense(gates, "gates", ids.shape, torch.float32)
+    wdt = _WEIGHTS[w_in.dtype]
+    if wdt == DMUON_I8:
+        if in_scale is None or out_scale is None:
+            raise ValueError("8-bit weights need in_scale and out_scale")
+        _dense(in_scale, "in_scale", (experts, n2), torch.float32)
+        _dense(out_scale, "out_scale", (experts, k), torch.float32)
+    elif in_scale is not None or out_scale is not None:
+        raise ValueError("in_scale and out_scale go with 8-bit weights")
+    device = _gpu(x)
+    if out is None:
+        out = _result(device, stream, (tokens, k), torch.bfloat16)
+    rows, cols, ldy = _rows2(out, "out")
+    if rows != tokens or cols != k or out.dtype != torch.bfloat16:
+        raise ValueError(f"out must be bfloat16, {tokens} x {k}")
+    _same_device(device, ids, gates, w_in, w_out, in_scale, out_scale, out, workspace)
+    d = dmuon_expert_layer_t(tokens, n, k, ldx, ldy, ld_in, ld_out, in_far, out_far, experts, ids.shape[1], wdt)
+    ws, wsb = _workspace(int(_lib.dmuon_expert_layer_workspace_size(d)), device, workspace, stream)
+    _launch(_lib.dmuon_expert_layer, "dmuon_expert_layer", device, stream, d, x.data_ptr(), ids.data_ptr(),
+            gates.data_ptr(), w_in.data_ptr(), in_scale.data_ptr() if in_scale is not None else None,
+            w_out.data_ptr(), out_scale.data_ptr() if out_scale is not None else None, out.data_ptr(),
+            ws.data_ptr() if ws is not None else None, wsb)
     return out
 
 

@@ -1,0 +1,257 @@
+// AdamW step with its two states in 8 bits, over every tensor of a call:
+//   m <- beta1 m + (1 - beta1) g
+//   v <- beta2 v + (1 - beta2) g^2
+//   p <- p (1 - lr wd) - (lr / (1 - beta1^t)) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+// m and r = sqrt(v) are held as e4m3 values with one fp32 scale per 128
+// consecutive elements (scale = max(amax / 448, 2^-126)), the second moment by
+// its root because its own range would be the square of what e4m3 has.
+// Between load and store everything is fp32.
+//
+// m is rounded to nearest even.  r is rounded at random, up with the
+// probability of the part cut off: a step moves v by (1 - beta2)(g^2 / v - 1)
+// of itself, 0.1 % with beta2 = 0.999, where neighbouring values of r^2 lie 13 to
+// 27 % apart, so that rounded to nearest it would keep the value it once had
+// (64 blocks of elements with gradients of fixed sizes that trade places half
+// way through 4000 steps: r over the true root 0.23 to 9.1, mean 0.76; rounded at random mean
+// 1.01, standard deviation 0.20).  m needs none of it: the gradient's own noise moves it by more than
+// its spacing.  The random number of element i is 16 bits of a hash of the
+// call's seed, the step, the tensor's place in the call and i / 2, so a step can
+// be repeated bit for bit; no multiplication and addition that r goes through
+// is fused, so any fp32 code can repeat it.
+#include "grouped.h"
+
+namespace dmuon {
+namespace {
+
+constexpr uint32_t kMinNormal = 121u << 23;      // exponent bits of e4m3's smallest normal number, 2^-6
+constexpr float kStateMax = 448.f;
+
+// Loads and stores of any alignment, not kept in the caches: every byte is
+// used once.
+typedef uint32_t any16_t __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t any8_t __attribute__((ext_vector_type(2), aligned(1)));
+#define DMUON_GLOBAL __attribute__((address_space(1)))
+template <class V>
+__device__ __forceinline__ V load_once(const void* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const DMUON_GLOBAL V*>(reinterpret_cast<uintptr_t>(p)));
+}
+template <class V>
+__device__ __forceinline__ void store_once(void* p, V v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<DMUON_GLOBAL V*>(reinterpret_cast<uintptr_t>(p)));
+}
+
+// Eight values of a real type from p on; the ones from `valid` on read as zero.
+__device__ __forceinline__ void load8(const char* p, bool bf16, int valid, float (&x)[8]) {
+  if (valid >= 8) {
+    if (bf16) {
+      const any16_t w = load_once<any16_t>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(w[e]);
+        x[2 * e + 1] = bf16_hi(w[e]);
+      }
+    } else {
+      const any16_t a = load_once<any16_t>(p), b = load_once<any16_t>(p + 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __uint_as_float(a[e]);
+        x[4 + e] = __uint_as_float(b[e]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = 0.f;
+      if (e < valid) x[e] = bf16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p)[e]) : reinterpret_cast<const float*>(p)[e];
+    }
+  }
+}
+__device__ __forceinline__ void store8(char* p, bool bf16, int valid, const float (&x)[8]) {
+  if (valid >= 8) {
+    if (bf16) {
+      store_once<any16_t>(p, any16_t{pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]), pack2_bf16(x[4], x[5]),
+                                     pack2_bf16(x[6], x[7])});
+    } else {
+      store_once<any16_t>(p, any16_t{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                     __float_as_uint(x[3])});
+      store_once<any16_t>(p + 16, any16_t{__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]),
+                                          __float_as_uint(x[7])});
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e >= valid) continue;
+      if (bf16) reinterpret_cast<uint16_t*>(p)[e] = uint16_t(pack2_bf16(x[e], 0.f));
+      else reinterpret_cast<float*>(p)[e] = x[e];
+    }
+  }
+}
+__device__ __forceinline__ u32x2_t load_state(const uint8_t* p, int valid) {
+  if (valid >= 8) return load_once<any8_t>(p);
+  u32x2_t w = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < valid) w[e >> 2] |= uint32_t(p[e]) << (8 * (e & 3));
+  return w;
+}
+__device__ __forceinline__ void store_state(uint8_t* p, int valid, u32x2_t w) {
+  if (valid >= 8) {
+    store_once<any8_t>(p, w);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < valid) p[e] = uint8_t(w[e >> 2] >> (8 * (e & 3)));
+}
+
+__device__ __forceinline__ void decode(u32x2_t w, float scale, float (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    x[4 * h + 0] = __builtin_amdgcn_cvt_f32_fp8(int(w[h]), 0) * scale;
+    x[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(int(w[h]), 1) * scale;
+    x[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(int(w[h]), 2) * scale;
+    x[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(int(w[h]), 3) * scale;
+  }
+}
+
+// The largest of sixteen lanes' values (rows of a wave).
+template <int CTRL>
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  uint32_t o = turned<0x128>(v);      // row_ror:8, 4, 2, 1
+  v = o > v ? o : v;
+  o = turned<0x124>(v);
+  v = o > v ? o : v;
+  o = turned<0x122>(v);
+  v = o > v ? o : v;
+  o = turned<0x121>(v);
+  return o > v ? o : v;
+}
+
+// Scale of the 128 values of sixteen lanes; the maximum is one of bit patterns,
+// where NaN > Inf > any number, so such a block gets a scale that is not finite.
+__device__ __forceinline__ float block_scale(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = __float_as_uint(x[e]) & 0x7fffffffu;
+    m = b > m ? b : m;
+  }
+  const float s = __uint_as_float(max16(m)) / kStateMax;
+  return s < 0x1p-126f ? 0x1p-126f : s;
+}
+
+__device__ __forceinline__ u32x2_t to_nearest(const float (&x)[8], float inv) {
+  u32x2_t w;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int q = 0;
+    q = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h] * inv, x[4 * h + 1] * inv, q, false);
+    q = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h + 2] * inv, x[4 * h + 3] * inv, q, true);
+    w[h] = uint32_t(q);
+  }
+  return w;
+}
+
+// A 32-bit hash: the finaliser of MurmurHash3 (A. Appleby, public domain) of x + 0x9e3779b9.
+__host__ __device__ inline uint32_t mix(uint32_t x) {
+  x += 0x9e3779b9u;
+  x = (x ^ (x >> 16)) * 0x85ebca6bu;
+  x = (x ^ (x >> 13)) * 0xc2b2ae35u;
+  return x ^ (x >> 16);
+}
+
+// y in 0 .. 448 to one of the two e4m3 values around it; u: 16 random bits.
+// With q the spacing at y, floor(y / q + u) counts steps of q from zero on; the
+// codes are those counts with 8 more per power of two above 2^-6.
+__device__ __forceinline__ uint32_t at_random(float y, uint32_t u) {
+  y = fminf(y, kStateMax);
+  const uint32_t bits = __float_as_uint(y) & 0x7f800000u;
+  const uint32_t exp = bits > kMinNormal ? bits : kMinNormal;
+  const float per = __uint_as_float((257u << 23) - exp);        // 1 / q
+  const uint32_t steps = uint32_t(fmaf(y, per, float(u) * 0x1p-16f));   // y * per is exact
+  return steps + ((exp - kMinNormal) >> 20);
+}
+
+// The kernel's argument (its only one) in place: indexed at run time it would
+// be copied to scratch memory.
+__device__ __forceinline__ const Adam8Table& table() {
+  auto* p = __builtin_amdgcn_kernarg_segment_ptr();
+  return *(const Adam8Table*)p;
+}
+
+// One block per 8192 elements of a tensor; a thread holds eight consecutive
+// elements at a time, sixteen lanes a block of 128.
+__global__ void __launch_bounds__(kAdam8Threads)
+adamw8_kernel(Adam8Table) {
+#pragma clang fp contract(off)
+  const Adam8Table& T = table();
+  int lo = 0, hi = T.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (T.items[mid].blk_first <= blockIdx.x) lo = mid; else hi = mid - 1;
+  }
+  const Adam8Item& it = T.items[lo];
+  const Adam8Group& G = T.groups[it.group];
+  const uint32_t chunk = blockIdx.x - it.blk_first;
+  const int64_t first = int64_t(chunk) * kAdam8Chunk;
+  const int count = int(it.numel - first < kAdam8Chunk ? it.numel - first : kAdam8Chunk);
+  const bool pbf = it.p_bf16, gbf = it.g_bf16;
+  char* const pp = static_cast<char*>(it.p) + first * (pbf ? 2 : 4);
+  const char* const gp = static_cast<const char*>(it.g) + first * (gbf ? 2 : 4);
+  uint8_t* const mp = it.m + first;
+  uint8_t* const rp = it.r + first;
+  float* const msp = it.m_scale + first / kAdam8Block;
+  float* const rsp = it.r_scale + first / kAdam8Block;
+  const uint32_t key = mix(it.key + it.chunk_first + chunk);
+  // whole blocks of 128: the lanes of one take part in its maximum together
+  const int padded = (count + kAdam8Block - 1) / kAdam8Block * kAdam8Block;
+  for (int e = int(threadIdx.x) * 8; e < padded; e += kAdam8Threads * 8) {
+    const int valid = count - e;
+    float p[8], g[8], m[8], r[8];
+    load8(pp + e * (pbf ? 2 : 4), pbf, valid, p);
+    load8(gp + e * (gbf ? 2 : 4), gbf, valid, g);
+    const u32x2_t mq = load_state(mp + e, valid), rq = load_state(rp + e, valid);
+    const float ms = msp[e / kAdam8Block], rs = rsp[e / kAdam8Block];
+    decode(mq, ms, m);
+    decode(rq, rs, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m[k] = G.beta1 * m[k] + G.one_minus_beta1 * g[k];
+      r[k] = sqrtf(G.beta2 * (r[k] * r[k]) + G.one_minus_beta2 * (g[k] * g[k]));
+      if (k >= valid) m[k] = r[k] = 0.f;
+      const float denom = fmaf(r[k], G.inv_sqrt_bc2, G.eps);
+      p[k] = fmaf(-G.step_size, m[k] / denom, p[k] * G.decay);
+    }
+    store8(pp + e * (pbf ? 2 : 4), pbf, valid, p);
+    const float ms_new = block_scale(m), rs_new = block_scale(r);
+    store_state(mp + e, valid, to_nearest(m, 1.f / ms_new));
+    const float inv = 1.f / rs_new;
+    u32x2_t w = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const uint32_t u = mix(key + uint32_t(e + k) / 2);
+      w[k >> 2] |= (at_random(r[k] * inv, u & 0xffffu) | at_random(r[k + 1] * inv, u >> 16) << 8) << (8 * (k & 3));
+    }
+    store_state(rp + e, valid, w);
+    if ((threadIdx.x & 15) == 0) {
+      msp[e / kAdam8Block] = ms_new;
+      rsp[e / kAdam8Block] = rs_new;
+    }
+  }
+}
+
+}  // namespace
+
+uint32_t adamw8_key(uint32_t seed, int64_t step, uint32_t tensor) {
+  return mix(mix(mix(seed) + uint32_t(step)) + tensor);
+}
+
+hipError_t launch_adamw8(const Adam8Table& table, int64_t nblocks, hipStream_t stream) {
+  hipLaunchKernelGGL(adamw8_kernel, dim3(static_cast<unsigned>(nblocks)), dim3(kAdam8Threads), 0, stream, table);
+  return hipGetLastError();
+}
+
+}  // namespace dmuon

@@ -840,7 +840,8 @@ int check_device() {
 const char* const kProfNames[PK_COUNT] = {"momentum", "finalize", "gemm_bf16", "gemm_f32", "update",
                                           "clip_norm", "clip_finalize", "clip_scale", "gram_sum",
                                           "adamw", "expert_bf16", "expert_f32", "quantize",
-                                          "dequantize", "block_matmul"};
+                                          "dequantize", "block_matmul", "adamw8", "quantize_rows",
+                                          "dequantize_rows", "int8_matmul", "layer_in", "layer_out"};
 
 struct ProfRec {
   int kind;

@@ -1,4 +1,7 @@
-// The 256 x 256 tile loop of the expert products in bf16.
+// The 256 x 256 tile loop of the expert products in bf16 and of the products of
+// 8-bit integers, whose stages have the same bytes: 128 k in place of 64, and
+// v_mfma_i32_16x16x64_i8 in place of v_mfma_f32_16x16x32_bf16, which takes as long.
+// Sums count in units of two bytes.
 //
 // C[i][j] = sum_s A(i, s) B(j, s), one block of four waves per CU.  A wave
 // computes 128 x 128 of the tile (16 x 16 blocks, of the rows every second
@@ -174,6 +177,7 @@ struct BigSlot {
 };
 
 constexpr int kBigStage = 64;             // s per stage
+constexpr int64_t kMaxBigPitch = int64_t(1) << 23;   // bytes: offsets of a tile's rows within 31 bits
 
 // The stream of one operand's loads: sixteen-byte pieces of a stage, eight
 // per lane, an eighth of the operand's rows apart, at fixed offsets (the row
@@ -257,23 +261,28 @@ __device__ __forceinline__ void wait_loads() {                                  
 __device__ __forceinline__ void big_mfma(f32x4_t& acc, const bf16x8_t& b, const bf16x8_t& a) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+// Sixteen 8-bit integers per lane and operand, int32 sums.
+__device__ __forceinline__ void big_mfma(i32x4_t& acc, const bf16x8_t& b, const bf16x8_t& a) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
 #define DMUON_ACC8(i) \
   "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]), "+a"(acc[i][4]), "+a"(acc[i][5]), \
       "+a"(acc[i][6]), "+a"(acc[i][7])
-template <int NI>
-__device__ __forceinline__ void settle(f32x4_t (&acc)[NI][8]) {
+template <int NI, typename Acc>
+__device__ __forceinline__ void settle(Acc (&acc)[NI][8]) {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : DMUON_ACC8(0));
 #pragma unroll
   for (int i = 1; i < NI; ++i) asm volatile("" : DMUON_ACC8(i));
   __builtin_amdgcn_sched_barrier(0);
 }
-template <int NI>
-__device__ __forceinline__ void clear(f32x4_t (&acc)[NI][8]) {
+template <int NI, typename Acc>
+__device__ __forceinline__ void clear(Acc (&acc)[NI][8]) {
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 8; ++j) acc[i][j] = Acc{0, 0, 0, 0};
   // opaque from here on, so that no zero is formed again next to its use
 #pragma unroll
   for (int i = 0; i < NI; ++i) asm volatile("s_nop 0" : DMUON_ACC8(i));
@@ -327,11 +336,30 @@ __device__ __forceinline__ void store_zeros(const BigWork& w, int wave, int lane
     for (int c = lane; c < w.cols; c += 64) reinterpret_cast<OutT*>(w.c + int64_t(r) * w.ldc)[c] = 0;
 }
 
+// What most operators share: fp32 accumulators that are stored as they are.
+template <typename OutT_>
+struct BigPlain {
+  using OutT = OutT_;
+  using Acc = f32x4_t;
+  using Work = BigWork;
+  static __device__ __forceinline__ void skip(BigWork*, int) {}
+  static __device__ __forceinline__ void to_scalar(BigWork*) {}
+  template <int NI>
+  static __device__ __forceinline__ void store(const BigWork& w, const f32x4_t (&acc)[NI][8], bool accumulate, int wave,
+                                               int lane) {
+    store_tile<OutT>(w, acc, accumulate, wave, lane);
+  }
+};
+
 // The tiles of one block.  Op: kColsA / kColsB (operand kinds), kShort (short
-// tiles happen), OutT, start(groups) -> number of tiles, find(position, work).
+// tiles happen), OutT, Acc (accumulators), Work (BigWork and what the operator
+// adds), start(groups) -> number of tiles, find(position, work), skip(work, rows)
+// and to_scalar(work) for what it adds, store(work, accumulators, ...).
 template <class Op>
 struct BigRun {
   using OutT = typename Op::OutT;
+  using Acc = typename Op::Acc;
+  using Work = typename Op::Work;
   static constexpr bool kA = Op::kColsA, kB = Op::kColsB;
 
   Op& op;
@@ -341,7 +369,7 @@ struct BigRun {
   const int lane0, wave;
   uint32_t pos;
   BigPlan plan;
-  BigWork w, nw;                 // present tile, next one (sum 0: none)
+  Work w, nw;                    // present tile, next one (sum 0: none)
   BigLoads<kA> la;               // the stage whose loads are being issued
   BigLoads<kB> lb;
   int loads_left;                // stages of its tile after it
@@ -355,7 +383,7 @@ struct BigRun {
   static __device__ __forceinline__ int stages_of(int sum) { return (sum + 2 * kBigStage - 1) / (2 * kBigStage) * 2; }
 
   // Tile or part of one at position p.
-  __device__ __forceinline__ void find(uint32_t p, BigWork* t) const {
+  __device__ __forceinline__ void find(uint32_t p, Work* t) const {
     uint32_t tile;
     int part;
     if (!plan.locate(p, &tile, &part)) {
@@ -368,17 +396,19 @@ struct BigRun {
       const int skip = plan.cut(part, &t->rows);
       t->a += int64_t(skip) * t->lda;
       t->c += int64_t(skip) * t->ldc;
+      Op::skip(t, skip);
       if (t->rows <= 0) t->sum = t->rows = 0;
     }
   }
   // The block's first tile from position p on that has anything to sum.
   // Tiles without are written here: zeros, or nothing when accumulating.
-  __device__ __forceinline__ void find_from(uint32_t p, BigWork* t) {
+  __device__ __forceinline__ void find_from(uint32_t p, Work* t) {
     t->sum = 0;
     t->rows = t->cols = 1;       // of no tile: loads that read nothing
     for (; p < plan.end; p += gridDim.x) {
       find(p, t);
       to_scalar(t);
+      Op::to_scalar(t);
       if (t->sum > 0) break;
       if (!accumulate) store_zeros<OutT>(*t, wave, here(lane0));
       t->sum = 0;
@@ -439,7 +469,7 @@ struct BigRun {
   // 1/RPART of them; loads L0 .. L1 - 1 of the running stage into LSLOT spread
   // over all of them.
   template <int NI, int SET, int HALF, int RSET, int RSLOT, int RPART, int LSLOT, int L0, int L1>
-  __device__ __forceinline__ void quarter(f32x4_t (&acc)[NI][8], int lane, int wv) {
+  __device__ __forceinline__ void quarter(Acc (&acc)[NI][8], int lane, int wv) {
     constexpr int NM = NI / 2 * 8, NR = RSET < 0 ? 0 : 8 + NI, LIM = NM / RPART, NL = L1 - L0;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
@@ -459,7 +489,7 @@ struct BigRun {
   }
   // One stage in SLOT; its step 0 is in registers.
   template <int NI, int SLOT>
-  __device__ __forceinline__ void stage(f32x4_t (&acc)[NI][8]) {
+  __device__ __forceinline__ void stage(Acc (&acc)[NI][8]) {
     const int lane = here(lane0), wv = here_scalar(wave);
     quarter<NI, 0, 0, 1, SLOT, 2, SLOT ^ 1, 14, 16>(acc, lane, wv);
     wait_lds();
@@ -476,7 +506,7 @@ struct BigRun {
   // The present tile, its first stage in slot 0 and visible.
   template <int NI>
   __device__ __forceinline__ void tile() {
-    f32x4_t acc[NI][8];
+    Acc acc[NI][8];
     clear(acc);
     const int stages = stages_of(w.sum);
     const int lane = here(lane0);
@@ -488,7 +518,7 @@ struct BigRun {
       stage<NI, 1>(acc);
     }
     settle(acc);
-    store_tile<OutT>(w, acc, accumulate, wave, here(lane0));
+    op.template store<NI>(w, acc, accumulate, wave, here(lane0));
   }
   __device__ __forceinline__ void run(BigGroups* groups) {
     plan.make(op.start(groups), Op::kShort);

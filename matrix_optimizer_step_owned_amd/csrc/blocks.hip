@@ -30,6 +30,7 @@
 //     sums, at half the rate.
 #include "bigtile.h"
 #include "skinny.h"
+#include "stage8.h"
 
 namespace dmuon {
 namespace {
@@ -307,37 +308,6 @@ dequantize_kernel(QuantArgs P) {
 
 // ---- product ----------------------------------------------------------------
 
-constexpr int kThreads = 256;
-
-// One thread's share of an operand's stage of 128 k: TILE / 32 chunks.
-template <int TILE, bool VEC>
-__device__ __forceinline__ void load_stage(const char* base, int64_t ld, int rows, int64_t k0, int64_t k,
-                                           u32x4_t (&v)[TILE / 32]) {
-  const int t = threadIdx.x;
-#pragma unroll
-  for (int q = 0; q < TILE / 32; ++q) {
-    const int r = (t >> 3) + 32 * q, c = (t & 7) * 16;
-    const int64_t left = k - k0 - c;
-    v[q] = load_chunk<1, VEC>(base + r * ld + k0 + c, r < rows ? int(left > 16 ? 16 : left) : 0);
-  }
-}
-template <int TILE>
-__device__ __forceinline__ void write_stage(char* lds, const u32x4_t (&v)[TILE / 32]) {
-  const int t = threadIdx.x;
-#pragma unroll
-  for (int q = 0; q < TILE / 32; ++q)
-    *reinterpret_cast<u32x4_t*>(lds + row_slot((t >> 3) + 32 * q, t & 7)) = v[q];
-}
-// A lane's 32 bytes of row r0 + lane % 16: chunks lane / 16 and lane / 16 + 4.
-// Which k a lane holds does not matter as long as both operands agree.
-__device__ __forceinline__ i32x8_t read_frag(const char* lds, int r0) {
-  const int lane = threadIdx.x & 63;
-  union { u32x4_t h[2]; i32x8_t v; } u;
-  u.h[0] = *reinterpret_cast<const u32x4_t*>(lds + row_slot(r0 + (lane & 15), lane >> 4));
-  u.h[1] = *reinterpret_cast<const u32x4_t*>(lds + row_slot(r0 + (lane & 15), 4 + (lane >> 4)));
-  return u.v;
-}
-
 template <bool E5M2>
 __device__ __forceinline__ bf16x2_t widen2(int w, bool hi) {
   if constexpr (E5M2)
@@ -379,7 +349,7 @@ __device__ __forceinline__ f32x4_t block_product(const i32x8_t& fb, const i32x8_
 // ring; any alignment.  fp32 results: every wave widens its fragments once per
 // stage, 4096 x 4096 x 8190 takes 368 us, 747 TFLOP/s.
 template <bool A5, bool B5, bool BROWS, bool VEC, int TILE, typename OutT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kStageThreads, 2)
 block_matmul_kernel(BlockArgs P) {
   constexpr bool EXACT = sizeof(OutT) == 4;
   constexpr int OPB = TILE * kBlk, D = TILE == 64 ? 4 : 1, F = TILE / 32;
@@ -529,7 +499,6 @@ block_matmul_kernel(BlockArgs P) {
 // 2.09 PFLOP/s; 8192 x 14336 x 4096: 467 us.
 constexpr int kWaves8 = 8;
 constexpr int kThreads8 = kWaves8 * 64;
-constexpr int64_t kMaxBigPitch = int64_t(1) << 23;
 
 struct BlockTile {
   const char* a;
@@ -839,7 +808,7 @@ __device__ __forceinline__ f32x4_t block_product_of(const i32x8_t& fb, const i32
 }
 
 template <bool EXACT>
-struct BlockSkinny {
+struct BlockSkinny : SkinnyFloat {
   const float* sa;      // of the tile's first row; kb per row
   const float* sb;      // of the tile's first column, or of its 128 columns
   int64_t kb;
@@ -933,7 +902,7 @@ hipError_t launch_skinny(const BlockArgs& P, int a5, int b5, int b_rows, bool f3
 
 template <bool A5, bool B5, bool BROWS, typename OutT>
 void launch_matmul(const BlockArgs& P, bool vec, bool small, dim3 grid, hipStream_t stream) {
-  const dim3 block(kThreads);
+  const dim3 block(kStageThreads);
   if (small) {
     if (vec) hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, true, 64, OutT>), grid, block, 0, stream, P);
     else hipLaunchKernelGGL((block_matmul_kernel<A5, B5, BROWS, false, 64, OutT>), grid, block, 0, stream, P);

@@ -249,9 +249,8 @@ expert_bf16_kernel(ExpertArgs P) {
 // ---- bf16, 256 x 256 tiles ----------------------------------------------------
 
 // Tiles and stages of an expert product for the 256-tile loop (bigtile.h).
-template <int OP, typename OutT_>
-struct ExpertBig {
-  using OutT = OutT_;
+template <int OP, typename OutT>
+struct ExpertBig : BigPlain<OutT> {
   static constexpr bool kColsA = OP == OP_WEIGHT, kColsB = OP != OP_FORWARD;
   static constexpr bool kShort = OP != OP_WEIGHT;     // rows of weights seldom end inside a tile
 
@@ -333,7 +332,7 @@ expert_bf16_big_kernel(ExpertArgs P) {
 
 // ---- bf16, few rows per expert (forward) ---------------------------------------
 
-struct ExpertSkinny {
+struct ExpertSkinny : SkinnyFloat {
   template <int MB, int NB>
   __device__ __forceinline__ void step(int, int, int, int, const SkinnyFrag (&b)[NB], const SkinnyFrag (&a)[MB],
                                        f32x4_t (&acc)[NB][MB]) const {

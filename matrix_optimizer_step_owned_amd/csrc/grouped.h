@@ -163,6 +163,11 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// silu(gate) * up; 1 + exp(-gate) may be Inf, which makes it zero.
+__device__ __forceinline__ float gated(float gate, float up) {
+  return gate * __builtin_amdgcn_rcpf(1.f + __expf(-gate)) * up;
+}
+
 // Sixteen bytes from p, of which the first `valid` elements of EB bytes are
 // inside the row; the others read as zero.  VEC: p is 16-byte aligned and
 // `valid` is either <= 0 or a whole chunk.  Without VEC a chunk that ends

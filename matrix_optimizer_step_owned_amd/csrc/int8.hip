@@ -1,0 +1,571 @@
+// 8-bit integers with one fp32 scale per row (a token, or an output channel of
+// a weight): quantisation, its inverse, and the matrix product of such operands.
+//
+// Quantising a row:
+//   scale = max(amax / 127, 2^-126),  q = rne(x * (1 / scale))
+// in fp32, so |q| <= 127; with a gated activation x = silu(gate) * up first, in
+// fp32 too.  The maximum is taken over the bit patterns of |x|, in which NaN >
+// Inf > any number: a row with a NaN or an Inf gets a scale that is not finite
+// and decodes to NaN, and no other row notices.
+//
+// Product: c[i][j] = a_scale[i] b_scale[j] * sum_k a[i][k] b[j][k].  The sum is
+// an exact int32 (k <= 131071: 2^14 per product), so neither its order nor its
+// split matters; it is converted to fp32 once, scaled by a row's and then by
+// a column's scale, and rounded once to bf16.  All forms use
+// v_mfma_i32_16x16x64_i8, whose peak is twice that of bf16.
+#include "bigtile.h"
+#include "skinny.h"
+#include "stage8.h"
+
+namespace dmuon {
+namespace {
+
+// ---- quantisation -----------------------------------------------------------
+
+constexpr float kIntMax = 127.f;
+constexpr float kScaleMin = 0x1p-126f;
+constexpr int kRowThreads = 256;
+
+struct __attribute__((packed, aligned(1))) AnyEight { u32x2_t v; };
+struct __attribute__((packed, aligned(2))) AnyHalves { u32x4_t v; };
+struct __attribute__((packed, aligned(4))) AnyWords { u32x4_t v; };
+
+// Eight consecutive values of a row; those from `valid` on are zero.
+template <bool F32>
+__device__ __forceinline__ void load8(const char* p, int valid, float (&x)[8]) {
+  if constexpr (F32) {
+    const u32x4_t a = load_chunk<4, false>(p, valid), b = load_chunk<4, false>(p + 16, valid - 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = __uint_as_float(a[e]);
+      x[4 + e] = __uint_as_float(b[e]);
+    }
+  } else {
+    const u32x4_t a = load_chunk<2, false>(p, valid);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = bf16_lo(a[e]);
+      x[2 * e + 1] = bf16_hi(a[e]);
+    }
+  }
+}
+
+// Eight values of row `row` from column `col` on (the values that are quantised).
+template <bool F32, bool GLU>
+__device__ __forceinline__ void row8(const RowsArgs& P, int64_t row, int64_t col, float (&x)[8]) {
+  constexpr int EB = F32 ? 4 : 2;
+  const int64_t left = P.cols - col;
+  const int valid = left < 0 ? 0 : left > 8 ? 8 : int(left);
+  const char* p = static_cast<const char*>(P.x) + (row * P.ldx + col) * EB;
+  load8<F32>(p, valid, x);
+  if constexpr (GLU) {
+    float up[8];
+    load8<F32>(p + P.cols * EB, valid, up);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = gated(x[e], up[e]);
+  }
+}
+
+__device__ __forceinline__ uint32_t max_bits(const float (&x)[8], uint32_t m) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = __float_as_uint(x[e]) & 0x7fffffffu;
+    m = b > m ? b : m;
+  }
+  return m;
+}
+
+// Four integers: x * inv + 1.5 * 2^23 holds the rounded value in its low byte.
+__device__ __forceinline__ uint32_t to_int8x4(const float* x, float inv) {
+#pragma clang fp contract(off)
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float y = x[e] * inv;
+    w[e] = __float_as_uint(y + 12582912.f);
+  }
+  const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(w[3], w[2], 0x04000c0cu);
+  return lo | hi;
+}
+
+__device__ __forceinline__ void store8(int8_t* q, int64_t left, const float (&x)[8], float inv) {
+  const u32x2_t w = {to_int8x4(x, inv), to_int8x4(x + 4, inv)};
+  if (left >= 8) {
+    reinterpret_cast<AnyEight*>(q)->v = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) q[e] = int8_t(w[e >> 2] >> (8 * (e & 3)));
+  }
+}
+
+// T threads take a row, eight columns each at a time; HELD such pieces stay in
+// registers between the maximum and the rounding (0: the row is read twice).
+template <bool F32, bool GLU, int T, int HELD>
+__global__ void __launch_bounds__(kRowThreads)
+quantize_rows_kernel(RowsArgs P) {
+  constexpr int PER = kRowThreads / T;      // rows of a block
+  __shared__ uint32_t wave_max[kRowThreads / 64];
+  const int t = threadIdx.x % T, wave = threadIdx.x >> 6;
+  for (int64_t base = int64_t(blockIdx.x) * PER; base < P.rows; base += int64_t(gridDim.x) * PER) {
+    const int64_t row = base + threadIdx.x / T;
+    const bool in = row < P.rows;
+    const int64_t last = in ? row : P.rows - 1;
+    float x[HELD > 0 ? HELD : 1][8];
+    uint32_t m = 0;
+    if constexpr (HELD > 0) {
+#pragma unroll
+      for (int h = 0; h < HELD; ++h) row8<F32, GLU>(P, last, int64_t(h * T + t) * 8, x[h]);
+#pragma unroll
+      for (int h = 0; h < HELD; ++h) m = max_bits(x[h], m);
+    } else {
+      for (int64_t col = t * 8; col < P.cols; col += T * 8) {
+        row8<F32, GLU>(P, last, col, x[0]);
+        m = max_bits(x[0], m);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_xor(m, d);
+      m = o > m ? o : m;
+    }
+    if constexpr (T > 64) {
+      __syncthreads();                      // the row before is done with them
+      if ((threadIdx.x & 63) == 0) wave_max[wave] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kRowThreads / 64; ++w) m = wave_max[w] > m ? wave_max[w] : m;
+    }
+    float scale = __uint_as_float(m) / kIntMax;
+    if (scale < kScaleMin) scale = kScaleMin;     // a NaN stays
+    const float inv = 1.f / scale;
+    if (!in) continue;                      // whole waves with T = 64, never with more
+    if (t == 0) P.scale[row] = scale;
+    int8_t* q = P.q + row * P.cols;
+    if constexpr (HELD > 0) {
+#pragma unroll
+      for (int h = 0; h < HELD; ++h) {
+        const int64_t col = int64_t(h * T + t) * 8;
+        if (col < P.cols) store8(q + col, P.cols - col, x[h], inv);
+      }
+    } else {
+      for (int64_t col = t * 8; col < P.cols; col += T * 8) {
+        row8<F32, GLU>(P, row, col, x[0]);
+        store8(q + col, P.cols - col, x[0], inv);
+      }
+    }
+  }
+}
+
+// q * scale in fp32, for bf16 then rounded; 64 threads take a row, 16 columns each at a time.
+template <bool F32>
+__global__ void __launch_bounds__(kRowThreads)
+dequantize_rows_kernel(RowsArgs P) {
+  const int t = threadIdx.x & 63;
+  const int64_t step = int64_t(gridDim.x) * (kRowThreads / 64);
+  for (int64_t row = int64_t(blockIdx.x) * (kRowThreads / 64) + (threadIdx.x >> 6); row < P.rows; row += step) {
+    const float s = P.scale[row];
+    const char* q = reinterpret_cast<const char*>(P.q) + row * P.cols;
+    char* out = static_cast<char*>(P.out) + row * P.ldx * (F32 ? 4 : 2);
+    for (int64_t col = t * 8; col < P.cols; col += 64 * 8) {
+      const int64_t left = P.cols - col;
+      const int valid = left > 8 ? 8 : int(left);
+      u32x2_t w = {0, 0};
+      if (valid == 8) {
+        w = reinterpret_cast<const AnyEight*>(q + col)->v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < valid) w[e >> 2] |= uint32_t(uint8_t(q[col + e])) << (8 * (e & 3));
+      }
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = float(int8_t(w[e >> 2] >> (8 * (e & 3)))) * s;
+      if constexpr (F32) {
+        float* p = reinterpret_cast<float*>(out) + col;
+        if (valid == 8) {
+          reinterpret_cast<AnyWords*>(p)[0].v = __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]});
+          reinterpret_cast<AnyWords*>(p)[1].v = __builtin_bit_cast(u32x4_t, f32x4_t{v[4], v[5], v[6], v[7]});
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < valid) p[e] = v[e];
+        }
+      } else {
+        uint16_t* p = reinterpret_cast<uint16_t*>(out) + col;
+        const u32x4_t h = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])};
+        if (valid == 8) {
+          reinterpret_cast<AnyHalves*>(p)->v = h;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < valid) p[e] = uint16_t(h[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+}
+
+constexpr int64_t kMaxRowBlocks = int64_t(1) << 20;     // blocks go on to further rows
+
+template <bool F32, bool GLU, int T>
+void launch_held(const RowsArgs& P, hipStream_t stream) {
+  const int64_t blocks = (P.rows + kRowThreads / T - 1) / (kRowThreads / T);
+  const dim3 grid(static_cast<unsigned>(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks)), block(kRowThreads);
+  const int64_t pieces = (P.cols + 8 * T - 1) / (8 * T);
+  if (pieces <= 1) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 1>), grid, block, 0, stream, P);
+  else if (pieces <= 2) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 2>), grid, block, 0, stream, P);
+  else if (pieces <= 4) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 4>), grid, block, 0, stream, P);
+  else if (pieces <= 8) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 8>), grid, block, 0, stream, P);
+  else if constexpr (T > 64) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 0>), grid, block, 0, stream, P);
+}
+
+// A wave per row where a wave holds a row and there are enough of them, else a block.
+template <bool F32, bool GLU>
+hipError_t launch_rows(const RowsArgs& P, hipStream_t stream) {
+  if (P.cols <= 64 * 8 * 8 && P.rows >= 1024) launch_held<F32, GLU, 64>(P, stream);
+  else launch_held<F32, GLU, kRowThreads>(P, stream);
+  return hipGetLastError();
+}
+
+// ---- product ----------------------------------------------------------------
+
+__device__ __forceinline__ i32x4_t multiply(const u32x4_t& b, const u32x4_t& a, const i32x4_t& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, b), __builtin_bit_cast(i32x4_t, a), c, 0, 0, 0);
+}
+
+// Scales of four consecutive columns of `cols`.
+__device__ __forceinline__ f32x4_t four_scales(const float* s, int col, int cols) {
+  struct __attribute__((packed, aligned(4))) Any { f32x4_t v; };
+  if (col + 4 <= cols) return reinterpret_cast<const Any*>(s + col)->v;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < cols) v[e] = s[col + e];
+  return v;
+}
+__device__ __forceinline__ f32x4_t scaled(const i32x4_t& sum, float sa, const f32x4_t& sb) {
+  return f32x4_t{float(sum[0]) * sa * sb[0], float(sum[1]) * sa * sb[1], float(sum[2]) * sa * sb[2],
+                 float(sum[3]) * sa * sb[3]};
+}
+
+// Tiles of 128 or 64, four waves in 2 x 2, operands staged through registers
+// and a two-slot LDS ring; any alignment.  Stages in flight as in block_matmul_kernel.
+template <bool VEC, int TILE, typename OutT>
+__global__ void __launch_bounds__(kStageThreads, 2)
+int8_matmul_kernel(Int8Args P) {
+  constexpr int kStep = 128;       // k per stage
+  constexpr int OPB = TILE * kStep, D = TILE == 64 ? 4 : 1, F = TILE / 32;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * OPB];
+  const uint32_t nt = (uint32_t(P.n) + TILE - 1) / TILE;
+  uint32_t mt;
+  if (P.offsets) mt = group_tiles(P.offsets, P.experts, int(P.m), TILE);
+  else mt = (uint32_t(P.m) + TILE - 1) / TILE;
+  const uint32_t pos = xcd_position(blockIdx.x, mt * nt);
+  if (pos >= mt * nt) return;
+  int tm, tn, row0, end, e = 0;
+  tile_of_position(pos, mt, nt, &tm, &tn);
+  if (P.offsets) {
+    const GroupSpan g = group_of_tile(P.offsets, P.experts, int(P.m), TILE, tm, &row0);
+    end = g.end;
+    e = g.expert;
+  } else {
+    row0 = tm * TILE;
+    end = int(P.m);
+  }
+  const int64_t j0 = int64_t(tn) * TILE;
+  const int rows = end - row0 < TILE ? end - row0 : TILE;
+  const int cols = int(P.n - j0 < TILE ? P.n - j0 : TILE);
+  const int stages = int((P.k + kStep - 1) / kStep);
+  const char* a = static_cast<const char*>(P.a) + row0 * P.lda;
+  const char* b = static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = (wave >> 1) * (TILE / 2), wn = (wave & 1) * (TILE / 2);
+  i32x4_t acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  u32x4_t va[D][TILE / 32], vb[D][TILE / 32];
+  auto load = [&](int st, int d) {
+    if (st < stages) {
+      load_stage<TILE, VEC>(a, P.lda, rows, int64_t(st) * kStep, P.k, va[d]);
+      load_stage<TILE, VEC>(b, P.ldb, cols, int64_t(st) * kStep, P.k, vb[d]);
+    }
+  };
+  auto write = [&](int st, int d) {
+    if (st < stages) {
+      write_stage<TILE>(smem + (st & 1) * 2 * OPB, va[d]);
+      write_stage<TILE>(smem + (st & 1) * 2 * OPB + OPB, vb[d]);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  write(0, 0);
+  load(D, 0);
+  for (int base = 0; base < stages; base += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int st = base + d;
+      if (st >= stages) break;
+      const char* cur = smem + (st & 1) * 2 * OPB;
+      __syncthreads();
+      write(st + 1, (d + 1) % D);
+      load(st + 1 + D, (d + 1) % D);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4_t fb[F];
+#pragma unroll
+        for (int j = 0; j < F; ++j) fb[j] = read_half(cur + OPB, wn + 16 * j, h);
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          const u32x4_t fa = read_half(cur, wm + 16 * i, h);
+#pragma unroll
+          for (int j = 0; j < F; ++j) acc[i][j] = multiply(fb[j], fa, acc[i][j]);
+        }
+      }
+    }
+  }
+  const float* sb = P.b_scale + e * P.n + j0;
+  const float* sa = P.a_scale + row0;
+#pragma unroll
+  for (int j = 0; j < F; ++j) {
+    const int col = wn + 16 * j + 4 * (lane >> 4);
+    const f32x4_t sc = four_scales(sb, col, cols);
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      const int r = wm + 16 * i + (lane & 15);
+      if (r >= rows) continue;
+      const f32x4_t x = scaled(acc[i][j], sa[r], sc);
+      const float v[4] = {x[0], x[1], x[2], x[3]};
+      store4<OutT>(static_cast<OutT*>(P.c) + (int64_t(row0) + r) * P.ldc + j0, col, cols, P.accumulate, v);
+    }
+  }
+}
+
+// ---- product, 256 x 256 tiles -------------------------------------------------
+
+struct Int8Work : BigWork {
+  const float* sa;       // of the tile's first row and column
+  const float* sb;
+};
+
+template <typename OutT_>
+struct Int8Big {
+  using OutT = OutT_;
+  using Acc = i32x4_t;
+  using Work = Int8Work;
+  static constexpr bool kColsA = false, kColsB = false, kShort = true;
+
+  const BigGroups* G;
+  uint32_t mt, nt;
+
+  // The kernel's arguments, read again at each use (Int8Args is its only parameter).
+  static __device__ __forceinline__ const Int8Args& args() {
+    auto* p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const Int8Args*)p;
+  }
+  __device__ __forceinline__ uint32_t start(BigGroups* g) {
+    const Int8Args& P = args();
+    G = g;
+    nt = (uint32_t(P.n) + kBig - 1) / kBig;
+    if (P.offsets) {
+      g->build(P.offsets, P.experts, int(P.m));
+      mt = uniform(g->tiles[P.experts]);
+    } else {
+      mt = (uint32_t(P.m) + kBig - 1) / kBig;
+    }
+    return mt * nt;
+  }
+  __device__ __forceinline__ void find(uint32_t pos, Int8Work* w) const {
+    const Int8Args& P = args();
+    int tm, tn, row0, end, e = 0;
+    tile_of_position(pos, mt, nt, &tm, &tn);
+    if (P.offsets) {
+      e = G->expert_of(P.experts, tm);
+      row0 = uniform(G->rows[e]) + (tm - uniform(G->tiles[e])) * kBig;
+      end = uniform(G->rows[e + 1]);
+    } else {
+      row0 = tm * kBig;
+      end = int(P.m);
+    }
+    const int64_t j0 = int64_t(tn) * kBig;
+    w->rows = end - row0 < kBig ? end - row0 : kBig;
+    w->cols = int(P.n - j0 < kBig ? P.n - j0 : kBig);
+    w->sum = int(P.k / 2);
+    w->lda = int(P.lda);
+    w->ldb = int(P.ldb);
+    w->ldc = int(P.ldc * int(sizeof(OutT)));
+    w->a = static_cast<const char*>(P.a) + row0 * P.lda;
+    w->b = static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb;
+    w->c = static_cast<char*>(P.c) + (row0 * P.ldc + j0) * int(sizeof(OutT));
+    w->sa = P.a_scale + row0;
+    w->sb = P.b_scale + e * P.n + j0;
+  }
+  static __device__ __forceinline__ void skip(Int8Work* w, int rows) { w->sa += rows; }
+  static __device__ __forceinline__ void to_scalar(Int8Work* w) {
+    w->sa = uniform_ptr(w->sa);
+    w->sb = uniform_ptr(w->sb);
+  }
+  // As store_tile, with the scales on the way.
+  template <int NI>
+  static __device__ __forceinline__ void store(const Int8Work& w, const i32x4_t (&acc)[NI][8], bool accumulate, int wave,
+                                               int lane) {
+    const int wm = wave >> 1, wn = wave & 1, g = lane >> 4;
+    const bool plain = !accumulate && w.cols == kBig;
+    f32x4_t sb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sb[j] = four_scales(w.sb, 128 * wn + 16 * j + 4 * g, w.cols);
+    float sa[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = 32 * i + 16 * wm + (lane & 15);
+      sa[i] = w.sa[r < w.rows ? r : w.rows - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = 32 * i + 16 * wm + (lane & 15);
+      OutT* row = reinterpret_cast<OutT*>(w.c + int64_t(r) * w.ldc) + 128 * wn;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const f32x4_t x = scaled(acc[i][j], sa[i], sb[j]), y = scaled(acc[i][j + 1], sa[i], sb[j + 1]);
+        if (sizeof(OutT) == 2 && plain) {
+          if constexpr (sizeof(OutT) == 2) store_pair(row + 16 * j, x, y, g, r < w.rows);
+        } else if (r < w.rows) {
+          const float u[4] = {x[0], x[1], x[2], x[3]}, v[4] = {y[0], y[1], y[2], y[3]};
+          store4<OutT>(row, 16 * j + 4 * g, w.cols - 128 * wn, accumulate, u);
+          store4<OutT>(row, 16 * (j + 1) + 4 * g, w.cols - 128 * wn, accumulate, v);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);   // one row of blocks at a time
+    }
+  }
+};
+
+template <typename OutT>
+__global__ void __launch_bounds__(kBigThreads)
+int8_matmul_big_kernel(Int8Args P) {
+  __shared__ BigSlot slot0, slot1;
+  __shared__ BigGroups groups;
+  Int8Big<OutT> op;
+  BigRun<Int8Big<OutT>> run(op, slot0.data, slot1.data, P.accumulate);
+  run.run(&groups);
+}
+
+// ---- product, few rows ----------------------------------------------------------
+
+struct Int8Skinny {
+  using Acc = i32x4_t;
+  const float* sa;      // of the tile's first row
+  const float* sb;      // of the tile's first column
+
+  template <int MB, int NB>
+  __device__ __forceinline__ void step(int, int, int, int, const SkinnyFrag (&b)[NB], const SkinnyFrag (&a)[MB],
+                                       i32x4_t (&acc)[NB][MB]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[n][m] = multiply(b[n].h[h], a[m].h[h], acc[n][m]);
+  }
+  __device__ __forceinline__ f32x4_t finish(const i32x4_t& v, int row, int col, int cols) const {
+    return scaled(v, sa[row], four_scales(sb, col, cols));
+  }
+};
+
+template <int MB, int NB, int W, typename OutT>
+__global__ void __launch_bounds__(64 * W)
+int8_skinny_kernel(Int8Args P) {
+  __shared__ __attribute__((aligned(16))) float sums[W * MB * NB * 256];
+  const uint32_t nt = (uint32_t(P.n) + 16 * NB - 1) / (16 * NB);
+  const uint32_t tm = blockIdx.x / nt, tn = blockIdx.x - tm * nt;
+  int row0 = int(tm) * 16 * MB, end = int(P.m), e = 0;
+  if (P.offsets) {
+    const GroupSpan g = group_of_tile(P.offsets, P.experts, int(P.m), 16 * MB, tm, &row0);
+    end = g.end;
+    e = g.expert;
+  }
+  if (row0 >= end) return;
+  const int64_t j0 = int64_t(tn) * (16 * NB);
+  const Int8Skinny op = {P.a_scale + row0, P.b_scale + e * P.n + j0};
+  skinny_block<Int8Skinny, MB, NB, W, OutT>(op, static_cast<const char*>(P.a) + row0 * P.lda, P.lda,
+                                            static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb, P.ldb,
+                                            static_cast<OutT*>(P.c) + row0 * P.ldc + j0, P.ldc,
+                                            end - row0 < 16 * MB ? end - row0 : 16 * MB,
+                                            int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k, P.accumulate, sums);
+}
+
+int64_t skinny_blocks(const Int8Args& P, int mb, int nb) {
+  const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
+  return (P.m / (16 * mb) + used) * ((P.n + 16 * nb - 1) / (16 * nb));
+}
+template <int MB, int NB, typename OutT>
+hipError_t launch_skinny(const Int8Args& P, hipStream_t stream) {
+  const int64_t blocks = skinny_blocks(P, MB, NB);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if constexpr (skinny_sixteen(MB, NB, sizeof(OutT) == 4)) {
+    if (blocks < kSkinnyWide) {
+      hipLaunchKernelGGL((int8_skinny_kernel<MB, NB, 16, OutT>), grid, dim3(1024), 0, stream, P);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((int8_skinny_kernel<MB, NB, 8, OutT>), grid, dim3(512), 0, stream, P);
+  return hipGetLastError();
+}
+
+template <typename OutT>
+hipError_t launch_matmul(const Int8Args& P, bool vec, hipStream_t stream) {
+  const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
+  const int64_t big = (P.m / kBig + used) * ((P.n + kBig - 1) / kBig);
+  // offsets of a tile's rows within 31 bits
+  const bool fits = P.lda <= kMaxBigPitch && P.ldb <= kMaxBigPitch && P.experts <= kBigExperts;
+  if (vec && fits && big >= 192) {
+    const dim3 grid(static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks)), block(kBigThreads);
+    hipLaunchKernelGGL((int8_matmul_big_kernel<OutT>), grid, block, 0, stream, P);
+    return hipGetLastError();
+  }
+  if (vec && skinny_blocks(P, 1, 1) <= kMaxSkinnyBlocks) {
+    // at most 16, or 32, rows per expert on average
+    const int64_t experts = P.offsets ? P.experts : 1;
+    if (P.m <= 16 * experts) {
+      if (skinny_blocks(P, 1, 2) >= kSkinnyWide) return launch_skinny<1, 2, OutT>(P, stream);
+      return launch_skinny<1, 1, OutT>(P, stream);
+    }
+    if (P.m <= 32 * experts) return launch_skinny<2, 2, OutT>(P, stream);
+  }
+  // 64-tiles where 128-tiles would give fewer than one per CU
+  auto tiles = [&](int64_t t) { return (P.m / t + used) * ((P.n + t - 1) / t); };
+  const bool small = tiles(128) < 256 && tiles(64) <= kMaxSkinnyBlocks;
+  const dim3 grid(static_cast<unsigned>(grouped_grid(tiles(small ? 64 : 128)))), block(kStageThreads);
+  if (small) {
+    if (vec) hipLaunchKernelGGL((int8_matmul_kernel<true, 64, OutT>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((int8_matmul_kernel<false, 64, OutT>), grid, block, 0, stream, P);
+  } else {
+    if (vec) hipLaunchKernelGGL((int8_matmul_kernel<true, 128, OutT>), grid, block, 0, stream, P);
+    else hipLaunchKernelGGL((int8_matmul_kernel<false, 128, OutT>), grid, block, 0, stream, P);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows(const RowsArgs& P, int x_dtype, hipStream_t stream) {
+  if (x_dtype == DT_F32) return P.glu ? launch_rows<true, true>(P, stream) : launch_rows<true, false>(P, stream);
+  return P.glu ? launch_rows<false, true>(P, stream) : launch_rows<false, false>(P, stream);
+}
+
+hipError_t launch_dequantize_rows(const RowsArgs& P, int x_dtype, hipStream_t stream) {
+  const int64_t blocks = (P.rows + kRowThreads / 64 - 1) / (kRowThreads / 64);
+  const dim3 grid(static_cast<unsigned>(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks)), block(kRowThreads);
+  if (x_dtype == DT_F32) hipLaunchKernelGGL((dequantize_rows_kernel<true>), grid, block, 0, stream, P);
+  else hipLaunchKernelGGL((dequantize_rows_kernel<false>), grid, block, 0, stream, P);
+  return hipGetLastError();
+}
+
+hipError_t launch_int8_matmul(const Int8Args& P, bool f32, bool vec, hipStream_t stream) {
+  return f32 ? launch_matmul<float>(P, vec, stream) : launch_matmul<uint16_t>(P, vec, stream);
+}
+
+}  // namespace dmuon

@@ -12,7 +12,7 @@
 
 namespace dmuon {
 
-enum : int32_t { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_E5M2 = 3 };
+enum : int32_t { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_E5M2 = 3, DT_I8 = 4 };
 
 // Edge of the square element tile of the elementwise kernels.
 constexpr int kEwTile = 64;
@@ -156,6 +156,41 @@ struct AdamItem {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamChunk = 8192;   // elements of one tensor per block
 
+// One tensor of an AdamW call with 8-bit states, its groups' constants, and
+// the tensors of one launch; the table travels as the kernel's argument.
+struct Adam8Item {
+  void* p;
+  const void* g;
+  uint8_t* m;            // e4m3
+  float* m_scale;        // one per 128 elements
+  uint8_t* r;            // e4m3, root of the second moment
+  float* r_scale;
+  int64_t numel;
+  uint32_t blk_first;    // first block of this tensor
+  uint32_t key;          // of its random numbers
+  uint16_t group;
+  uint8_t p_bf16, g_bf16;
+  uint32_t chunk_first;  // chunks of the tensor in earlier launches
+};
+struct Adam8Group {      // as AdamItem has them
+  float decay, step_size, inv_sqrt_bc2, eps;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+};
+constexpr int kAdam8Threads = 256;
+constexpr int kAdam8Chunk = 8192;      // elements of one tensor per block
+constexpr int kAdam8Block = 128;       // elements per scale
+constexpr int kAdam8Tensors = 40;      // of one launch: a table of 3.4 KB
+constexpr int kAdam8Groups = 16;
+constexpr int64_t kMaxAdam8Blocks = int64_t(1) << 23;   // of one launch: fewer than 2^32 threads
+struct Adam8Table {
+  Adam8Item items[kAdam8Tensors];
+  Adam8Group groups[kAdam8Groups];
+  int32_t n;
+};
+// Key of a tensor's random numbers.
+uint32_t adamw8_key(uint32_t seed, int64_t step, uint32_t tensor);
+hipError_t launch_adamw8(const Adam8Table& table, int64_t nblocks, hipStream_t stream);
+
 // fp64 -> fp32 rounded to odd: truncate, then set the last bit when inexact.
 // A value rounded to odd at 24 bits and then to nearest-even at 8 bits is the
 // nearest-even rounding of the fp64 value itself (24 >= 2 * 8 + 2), so a bf16
@@ -217,10 +252,56 @@ struct BlockArgs {
 hipError_t launch_block_matmul(const BlockArgs& P, int a_dtype, int b_dtype, bool brows, bool f32, bool vec,
                                hipStream_t stream);
 
+// ---- 8-bit integers and the expert layer (int8.hip, layer.hip) --------------
+
+struct RowsArgs {
+  const void* x;             // quantise: rows x cols, or rows x 2 cols (gate, up)
+  void* out;                 // dequantise: destination, ldx apart
+  int8_t* q;
+  float* scale;
+  int64_t rows, cols, ldx;
+  int32_t glu;
+};
+hipError_t launch_quantize_rows(const RowsArgs& P, int x_dtype, hipStream_t stream);
+hipError_t launch_dequantize_rows(const RowsArgs& P, int x_dtype, hipStream_t stream);
+
+struct Int8Args {
+  const void* a;
+  const void* b;
+  const float* a_scale;      // m
+  const float* b_scale;      // n, or experts x n
+  void* c;
+  const int32_t* offsets;    // null: one product
+  int64_t m, n, k, lda, ldb, ldc, b_stride;
+  int32_t experts;
+  int32_t accumulate;
+};
+hipError_t launch_int8_matmul(const Int8Args& P, bool f32, bool vec, hipStream_t stream);
+
+constexpr int kLayerTokens = 64;       // most tokens, picks of a token and experts of a layer call
+constexpr int kLayerPicks = 64;
+constexpr int kLayerExperts = 4096;
+struct LayerArgs {
+  const void* x;
+  const int32_t* ids;        // tokens x top_k
+  const float* gates;        // tokens x top_k
+  const void* w_in;          // experts x 2n x k
+  const float* in_scale;     // experts x 2n, or null (bf16 weights)
+  const void* w_out;         // experts x k x n
+  const float* out_scale;    // experts x k, or null
+  void* y;
+  uint16_t* h;               // workspace: tokens * top_k rows of n bf16
+  int64_t n, k, ldx, ldy, ld_in, ld_out, in_stride, out_stride;
+  int32_t tokens, experts, top_k;
+};
+hipError_t launch_layer_in(const LayerArgs& P, bool vec, hipStream_t stream);
+hipError_t launch_layer_out(const LayerArgs& P, bool vec, hipStream_t stream);
+
 // Kernel kinds of the profiling report.
 enum ProfKind { PK_MOMENTUM, PK_FINALIZE, PK_GEMM_BF16, PK_GEMM_F32, PK_UPDATE,
                 PK_CLIP_NORM, PK_CLIP_FINALIZE, PK_CLIP_SCALE, PK_GRAM_SUM, PK_ADAMW,
-                PK_EXPERT_BF16, PK_EXPERT_F32, PK_QUANTIZE, PK_DEQUANTIZE, PK_BLOCK_MATMUL, PK_COUNT };
+                PK_EXPERT_BF16, PK_EXPERT_F32, PK_QUANTIZE, PK_DEQUANTIZE, PK_BLOCK_MATMUL,
+                PK_ADAMW8, PK_QUANTIZE_ROWS, PK_DEQUANTIZE_ROWS, PK_INT8_MATMUL, PK_LAYER_IN, PK_LAYER_OUT, PK_COUNT };
 
 // DMUON_OK when the current device is a gfx950, else the error's status.
 int check_current_device();

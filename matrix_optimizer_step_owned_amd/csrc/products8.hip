@@ -1,0 +1,340 @@
+// Entry points of the operators on 8-bit states, 8-bit integers and of the
+// expert layer: argument checks and launches.  Nothing is staged in memory (the
+// arguments travel with the launch), so these calls may be captured into a graph.
+#include <algorithm>
+#include <cmath>
+#include <exception>
+#include <vector>
+
+#include "checks.h"
+
+namespace dmuon {
+namespace {
+
+// What a call holds in memory of its own (a std::bad_alloc must not leave a C function).
+template <class F>
+int guarded(F f) {
+  try {
+    set_last_error("");
+    return f();
+  } catch (const std::exception&) {
+    return set_last_error(DMUON_ERR_INVALID_ARG, "no host memory");
+  }
+}
+
+struct Written {
+  uintptr_t lo, hi;
+  int32_t tensor;
+  int32_t what;
+};
+const char* const kStateNames[] = {"param", "grad", "exp_avg", "exp_avg_scale", "root", "root_scale"};
+
+std::string state_name(int i, int what = -1) {
+  return "tensors[" + std::to_string(i) + "]" + (what < 0 ? "" : std::string(".") + kStateNames[what]);
+}
+
+int adamw8_step(const dmuon_adamw_quantized_t* tensors, int32_t n, const dmuon_adamw_group_t* groups, int32_t ngroups,
+                uint32_t seed, void* stream_) {
+  if (n < 0) return bad("n < 0");
+  if (n == 0) return DMUON_OK;
+  if (!tensors) return bad("tensors is NULL");
+  if (ngroups < 1 || !groups) return bad("ngroups must be >= 1 and groups non-NULL");
+  std::vector<Adam8Group> folded(ngroups);
+  for (int k = 0; k < ngroups; ++k) {
+    const dmuon_adamw_group_t& G = groups[k];
+    auto wrong = [k](const char* what) { return bad("groups[" + std::to_string(k) + "]: " + what); };
+    if (!std::isfinite(G.lr) || !std::isfinite(G.weight_decay)) return wrong("lr and weight_decay must be finite");
+    if (!std::isfinite(G.eps) || G.eps < 0) return wrong("eps must be finite and >= 0");
+    if (!(G.beta1 >= 0 && G.beta1 < 1) || !(G.beta2 >= 0 && G.beta2 < 1)) return wrong("betas must be in [0, 1)");
+    if (G.step < 1) return wrong("step must be >= 1");
+    const double t = static_cast<double>(G.step);
+    const double bc1 = 1.0 - std::pow(G.beta1, t), bc2 = 1.0 - std::pow(G.beta2, t);
+    Adam8Group& f = folded[k];
+    f.decay = static_cast<float>(1.0 - G.lr * G.weight_decay);
+    f.step_size = static_cast<float>(G.lr / bc1);
+    f.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
+    f.eps = static_cast<float>(G.eps);
+    f.beta1 = static_cast<float>(G.beta1);
+    f.one_minus_beta1 = static_cast<float>(1.0 - G.beta1);
+    f.beta2 = static_cast<float>(G.beta2);
+    f.one_minus_beta2 = static_cast<float>(1.0 - G.beta2);
+  }
+  std::vector<int> active;
+  std::vector<Written> spans;
+  active.reserve(n);
+  spans.reserve(6 * size_t(n));
+  for (int i = 0; i < n; ++i) {
+    const dmuon_adamw_quantized_t& T = tensors[i];
+    if (T.numel < 0 || T.numel > kMaxNumel) return bad(state_name(i) + ".numel must be in 0..2^42");
+    if (T.group < 0 || T.group >= ngroups) return bad(state_name(i) + ".group out of range");
+    if (!real_dtype(T.param_dtype) || !real_dtype(T.grad_dtype))
+      return set_last_error(DMUON_ERR_UNSUPPORTED, state_name(i) + ": dtypes must be F32 or BF16");
+    if (T.numel == 0 || !T.grad) continue;
+    if (!T.param || !T.exp_avg || !T.exp_avg_scale || !T.root || !T.root_scale)
+      return bad(state_name(i) + ": param and states must be non-NULL");
+    if (!aligned(T.param, size_of(T.param_dtype)) || !aligned(T.grad, size_of(T.grad_dtype)) ||
+        !aligned(T.exp_avg_scale, 4) || !aligned(T.root_scale, 4))
+      return bad(state_name(i) + ": a buffer is not aligned to its element");
+    active.push_back(i);
+    const void* p[6] = {T.param, T.grad, T.exp_avg, T.exp_avg_scale, T.root, T.root_scale};
+    const int64_t scales = 4 * up(T.numel, kAdam8Block);
+    const int64_t bytes[6] = {T.numel * size_of(T.param_dtype), T.numel * size_of(T.grad_dtype), T.numel, scales,
+                              T.numel, scales};
+    for (int w = 0; w < 6; ++w) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(p[w]);
+      spans.push_back({lo, lo + uintptr_t(bytes[w]), i, w});
+    }
+  }
+  if (active.empty()) return DMUON_OK;
+  std::sort(spans.begin(), spans.end(), [](const Written& a, const Written& b) { return a.lo < b.lo; });
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i].lo < spans[i - 1].hi)
+      return set_last_error(DMUON_ERR_ALIASING, state_name(spans[i - 1].tensor, spans[i - 1].what) + " overlaps " +
+                                                    state_name(spans[i].tensor, spans[i].what));
+  int st = check_current_device();
+  if (st) return st;
+  const hipStream_t stream = static_cast<hipStream_t>(stream_);
+  // as many launches as their tables need
+  size_t next = 0;
+  int64_t tail = 0;       // elements of tensors[active[next]] that earlier launches took
+  while (next < active.size()) {
+    Adam8Table table;
+    int ngr = 0, used[kAdam8Groups];
+    int64_t blocks = 0, bytes = 0;
+    table.n = 0;
+    for (; next < active.size() && table.n < kAdam8Tensors && blocks < kMaxAdam8Blocks; ) {
+      const int i = active[next];
+      const dmuon_adamw_quantized_t& T = tensors[i];
+      int g = 0;
+      while (g < ngr && used[g] != T.group) ++g;
+      if (g == ngr) {
+        if (ngr == kAdam8Groups) break;
+        used[ngr] = T.group;
+        table.groups[ngr++] = folded[T.group];
+      }
+      const int64_t all = up(T.numel - tail, kAdam8Chunk), some = std::min(all, kMaxAdam8Blocks - blocks);
+      Adam8Item& it = table.items[table.n++];
+      it.p = static_cast<char*>(T.param) + tail * size_of(T.param_dtype);
+      it.g = static_cast<const char*>(T.grad) + tail * size_of(T.grad_dtype);
+      it.m = static_cast<uint8_t*>(T.exp_avg) + tail;
+      it.m_scale = T.exp_avg_scale + tail / kAdam8Block;
+      it.r = static_cast<uint8_t*>(T.root) + tail;
+      it.r_scale = T.root_scale + tail / kAdam8Block;
+      it.numel = some < all ? some * kAdam8Chunk : T.numel - tail;
+      it.blk_first = static_cast<uint32_t>(blocks);
+      it.key = adamw8_key(seed, groups[T.group].step, static_cast<uint32_t>(i));
+      it.chunk_first = static_cast<uint32_t>(tail / kAdam8Chunk);
+      it.group = static_cast<uint16_t>(g);
+      it.p_bf16 = T.param_dtype == DT_BF16;
+      it.g_bf16 = T.grad_dtype == DT_BF16;
+      blocks += some;
+      bytes += it.numel * (2 * size_of(T.param_dtype) + size_of(T.grad_dtype) + 4) + it.numel / kAdam8Block * 16;
+      if (some < all) {
+        tail += it.numel;
+      } else {
+        tail = 0;
+        ++next;
+      }
+    }
+    st = hip_status(profiled_launch(PK_ADAMW8, 0, bytes, stream, [&] { return launch_adamw8(table, blocks, stream); }),
+                    "adamw_step_quantized");
+    if (st) return st;
+  }
+  return DMUON_OK;
+}
+
+int check_rows(const dmuon_rows_t* d) {
+  if (!d) return bad("rows descriptor is NULL");
+  if (d->rows < 0 || d->rows > kMaxRows) return bad("rows must be in 0..2^30");
+  if (d->cols < 1 || d->cols > kMaxDim) return bad("cols must be in 1..2^22");
+  if (d->activation != DMUON_ACT_NONE && d->activation != DMUON_ACT_SWIGLU) return bad("unknown activation");
+  const int64_t wide = d->cols * (d->activation == DMUON_ACT_SWIGLU ? 2 : 1);
+  if (d->ldx < wide || d->ldx > 2 * kMaxDim) return bad("ldx must be at least a row of x and at most 2^23");
+  if (!real_dtype(d->x_dtype)) return set_last_error(DMUON_ERR_UNSUPPORTED, "x_dtype must be F32 or BF16");
+  return DMUON_OK;
+}
+
+int check_layer(const dmuon_expert_layer_t* d) {
+  if (!d) return bad("layer descriptor is NULL");
+  if (d->tokens < 0 || d->tokens > kLayerTokens)
+    return bad("tokens must be in 0..64 (more: dmuon_expert_matmul or dmuon_row_matmul)");
+  if (d->n < 1 || d->n > kMaxDim || d->k < 1 || d->k > kMaxDim) return bad("n and k must be in 1..2^22");
+  if (d->experts < 1 || d->experts > kLayerExperts) return bad("experts must be in 1..4096");
+  if (d->top_k < 1 || d->top_k > kLayerPicks) return bad("top_k must be in 1..64");
+  return DMUON_OK;
+}
+
+}  // namespace
+}  // namespace dmuon
+
+using namespace dmuon;
+
+extern "C" {
+
+int dmuon_adamw_step_quantized(const dmuon_adamw_quantized_t* tensors, int32_t n, const dmuon_adamw_group_t* groups,
+                      int32_t ngroups, uint32_t seed, void* stream) {
+  return guarded([&] { return adamw8_step(tensors, n, groups, ngroups, seed, stream); });
+}
+
+int dmuon_quantize_rows(const dmuon_rows_t* d, const void* x, void* q, float* scale, void* stream_) {
+  return guarded([&]() -> int {
+    int st = check_rows(d);
+    if (st) return st;
+    if (d->rows == 0) return DMUON_OK;
+    if (!x || !q || !scale) return bad("a buffer is NULL");
+    const int64_t xs = size_of(d->x_dtype), wide = d->cols * (d->activation == DMUON_ACT_SWIGLU ? 2 : 1);
+    if (!aligned(x, xs) || !aligned(scale, 4)) return bad("a buffer is not aligned to its element");
+    const int64_t n = d->rows * d->cols;
+    st = check_spans({{q, n, "q"}, {scale, 4 * d->rows, "scale"}, {x, rows_bytes(d->rows, d->ldx, wide, xs), "x"}}, 2);
+    if (st) return st;
+    st = check_current_device();
+    if (st) return st;
+    RowsArgs P = {};
+    P.x = x; P.q = static_cast<int8_t*>(q); P.scale = scale;
+    P.rows = d->rows; P.cols = d->cols; P.ldx = d->ldx;
+    P.glu = d->activation == DMUON_ACT_SWIGLU;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_);
+    return hip_status(profiled_launch(PK_QUANTIZE_ROWS, 3 * n, d->rows * wide * xs + n, stream,
+                                      [&] { return launch_quantize_rows(P, d->x_dtype, stream); }),
+                      "quantize_rows");
+  });
+}
+
+int dmuon_dequantize_rows(const dmuon_rows_t* d, const void* q, const float* scale, void* x, void* stream_) {
+  return guarded([&]() -> int {
+    int st = check_rows(d);
+    if (st) return st;
+    if (d->activation != DMUON_ACT_NONE) return bad("an activation has no inverse");
+    if (d->rows == 0) return DMUON_OK;
+    if (!x || !q || !scale) return bad("a buffer is NULL");
+    const int64_t xs = size_of(d->x_dtype), n = d->rows * d->cols;
+    if (!aligned(x, xs) || !aligned(scale, 4)) return bad("a buffer is not aligned to its element");
+    st = check_spans({{x, rows_bytes(d->rows, d->ldx, d->cols, xs), "x"}, {q, n, "q"}, {scale, 4 * d->rows, "scale"}}, 1);
+    if (st) return st;
+    st = check_current_device();
+    if (st) return st;
+    RowsArgs P = {};
+    P.out = x; P.q = static_cast<int8_t*>(const_cast<void*>(q)); P.scale = const_cast<float*>(scale);
+    P.rows = d->rows; P.cols = d->cols; P.ldx = d->ldx;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_);
+    return hip_status(profiled_launch(PK_DEQUANTIZE_ROWS, n, n * (xs + 1), stream,
+                                      [&] { return launch_dequantize_rows(P, d->x_dtype, stream); }),
+                      "dequantize_rows");
+  });
+}
+
+int dmuon_row_matmul(const dmuon_row_product_t* d, const void* a, const float* a_scale, const void* b,
+                      const float* b_scale, const int32_t* offsets, void* c, void* stream_) {
+  return guarded([&]() -> int {
+    if (!d) return bad("product descriptor is NULL");
+    if (d->m < 0 || d->m > kMaxRows) return bad("m must be in 0..2^30");
+    if (d->n < 1 || d->n > kMaxDim) return bad("n must be in 1..2^22");
+    if (d->k < 1 || d->k > kMaxInt8Sum) return bad("k must be in 1..131071 (the sum is an int32)");
+    if (d->experts < 0 || d->experts > kMaxExperts) return bad("experts must be in 0..65536");
+    if ((d->experts > 0) != (offsets != nullptr)) return bad("offsets go with experts > 0");
+    if (d->lda < d->k || d->lda > kMaxRows || d->ldb < d->k || d->ldb > kMaxRows || d->ldc < d->n || d->ldc > kMaxDim)
+      return bad("row strides must be at least the row and at most 2^30 (a, b) or 2^22 (c)");
+    if (d->experts > 1 && (d->b_stride < (d->n - 1) * d->ldb + d->k || d->b_stride > kMaxStride))
+      return bad("b_stride must be at least one expert's weights and at most 2^44");
+    if (d->accumulate != 0 && d->accumulate != 1) return bad("accumulate must be 0 or 1");
+    if (!real_dtype(d->out_dtype)) return set_last_error(DMUON_ERR_UNSUPPORTED, "out_dtype must be F32 or BF16");
+    if (d->m == 0) return DMUON_OK;
+    if (!a || !a_scale || !b || !b_scale || !c) return bad("a buffer is NULL");
+    const int64_t osz = size_of(d->out_dtype), ne = d->experts > 0 ? d->experts : 1;
+    if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(c, osz) || !aligned(offsets, 4))
+      return bad("a buffer is not aligned to its element");
+    const int64_t ab = rows_bytes(d->m, d->lda, d->k, 1);
+    const int64_t bb = (ne - 1) * d->b_stride + rows_bytes(d->n, d->ldb, d->k, 1);
+    const int64_t cbytes = rows_bytes(d->m, d->ldc, d->n, osz);
+    int st = check_spans({{c, cbytes, "c"}, {a, ab, "a"}, {b, bb, "b"}, {a_scale, 4 * d->m, "a_scale"},
+                          {b_scale, 4 * ne * d->n, "b_scale"}, {offsets, 4 * (int64_t(d->experts) + 1), "offsets"}}, 1);
+    if (st) return st;
+    const int64_t used = d->experts > 0 ? (d->experts < d->m ? d->experts : d->m) : 1;
+    if ((d->m / 128 + used) * up(d->n, 128) > kMaxBlocks)
+      return set_last_error(DMUON_ERR_UNSUPPORTED, "more than 2^24 tiles of 128 x 128");
+    st = check_current_device();
+    if (st) return st;
+    Int8Args P = {};
+    P.a = a; P.b = b; P.a_scale = a_scale; P.b_scale = b_scale; P.c = c; P.offsets = offsets;
+    P.m = d->m; P.n = d->n; P.k = d->k; P.lda = d->lda; P.ldb = d->ldb; P.ldc = d->ldc;
+    P.b_stride = ne > 1 ? d->b_stride : 0;
+    P.experts = d->experts; P.accumulate = d->accumulate;
+    const bool vec = aligned(a, 16) && aligned(b, 16) && d->k % 16 == 0 && d->lda % 16 == 0 && d->ldb % 16 == 0 &&
+                     P.b_stride % 16 == 0;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_);
+    return hip_status(profiled_launch(PK_INT8_MATMUL, product_flops(d->m, d->n, d->k), ab + bb + cbytes, stream,
+                                      [&] { return launch_int8_matmul(P, d->out_dtype == DT_F32, vec, stream); }),
+                      "row_matmul");
+  });
+}
+
+size_t dmuon_expert_layer_workspace_size(const dmuon_expert_layer_t* d) {
+  if (!d || d->tokens < 1 || d->tokens > kLayerTokens || d->top_k < 1 || d->top_k > kLayerPicks || d->n < 1 ||
+      d->n > kMaxDim)
+    return 0;
+  return static_cast<size_t>(d->tokens * d->top_k * up(d->n, 8) * 16);
+}
+
+int dmuon_expert_layer(const dmuon_expert_layer_t* d, const void* x, const int32_t* ids, const float* gates,
+                       const void* w_in, const float* in_scale, const void* w_out, const float* out_scale, void* y,
+                       void* workspace, size_t workspace_bytes, void* stream_) {
+  return guarded([&]() -> int {
+    int st = check_layer(d);
+    if (st) return st;
+    const bool i8 = d->weight_dtype == DMUON_I8;
+    if (!i8 && d->weight_dtype != DMUON_BF16)
+      return set_last_error(DMUON_ERR_UNSUPPORTED, "weight_dtype must be BF16 or I8");
+    if (d->ldx < d->k || d->ldx > kMaxDim || d->ldy < d->k || d->ldy > kMaxDim || d->ld_in < d->k || d->ld_in > kMaxDim ||
+        d->ld_out < d->n || d->ld_out > kMaxDim)
+      return bad("row strides must be at least the row and at most 2^22");
+    const int64_t in_rows = 2 * d->n, in_all = (in_rows - 1) * d->ld_in + d->k, out_all = (d->k - 1) * d->ld_out + d->n;
+    if (d->experts > 1 && (d->in_stride < in_all || d->in_stride > kMaxStride || d->out_stride < out_all ||
+                           d->out_stride > kMaxStride))
+      return bad("in_stride and out_stride must be at least one expert's weights and at most 2^44");
+    if (d->tokens == 0) return DMUON_OK;
+    if (!x || !ids || !gates || !w_in || !w_out || !y) return bad("a buffer is NULL");
+    if (i8 != (in_scale != nullptr) || i8 != (out_scale != nullptr))
+      return bad("in_scale and out_scale go with 8-bit weights");
+    const int64_t ws = i8 ? 1 : 2;
+    if (!aligned(x, 2) || !aligned(y, 2) || !aligned(w_in, ws) || !aligned(w_out, ws) || !aligned(ids, 4) ||
+        !aligned(gates, 4) || !aligned(in_scale, 4) || !aligned(out_scale, 4))
+      return bad("a buffer is not aligned to its element");
+    const int64_t picks = d->tokens * d->top_k, need = static_cast<int64_t>(dmuon_expert_layer_workspace_size(d));
+    if (!workspace || workspace_bytes < static_cast<size_t>(need))
+      return set_last_error(DMUON_ERR_WORKSPACE, "workspace too small");
+    if (!aligned(workspace, 16)) return bad("workspace must be 16-byte aligned");
+    const int64_t in_stride = d->experts > 1 ? d->in_stride : 0, out_stride = d->experts > 1 ? d->out_stride : 0;
+    const int64_t ib = ((d->experts - 1) * in_stride + in_all) * ws, ob = ((d->experts - 1) * out_stride + out_all) * ws;
+    st = check_spans({{y, rows_bytes(d->tokens, d->ldy, d->k, 2), "y"}, {workspace, need, "the workspace"},
+                      {x, rows_bytes(d->tokens, d->ldx, d->k, 2), "x"}, {ids, 4 * picks, "ids"}, {gates, 4 * picks, "gates"},
+                      {w_in, ib, "w_in"}, {w_out, ob, "w_out"}, {in_scale, 4 * d->experts * in_rows, "in_scale"},
+                      {out_scale, 4 * d->experts * d->k, "out_scale"}}, 2);
+    if (st) return st;
+    const int64_t slots = picks < d->experts ? picks : d->experts;
+    if (slots * up(d->n, 16) > (int64_t(1) << 22))
+      return set_last_error(DMUON_ERR_UNSUPPORTED, "more than 2^22 pieces of 16 columns");
+    st = check_current_device();
+    if (st) return st;
+    LayerArgs P = {};
+    P.x = x; P.ids = ids; P.gates = gates; P.w_in = w_in; P.in_scale = in_scale; P.w_out = w_out; P.out_scale = out_scale;
+    P.y = y; P.h = static_cast<uint16_t*>(workspace);
+    P.n = d->n; P.k = d->k; P.ldx = d->ldx; P.ldy = d->ldy; P.ld_in = d->ld_in; P.ld_out = d->ld_out;
+    P.in_stride = in_stride; P.out_stride = out_stride;
+    P.tokens = static_cast<int32_t>(d->tokens); P.experts = d->experts; P.top_k = d->top_k;
+    // whole 16-byte chunks along every row
+    const bool vec = aligned(x, 16) && aligned(w_in, 16) && aligned(w_out, 16) && d->ldx % 8 == 0 &&
+                     d->k * ws % 16 == 0 && d->n * ws % 16 == 0 && d->ld_in * ws % 16 == 0 && d->ld_out * ws % 16 == 0 &&
+                     in_stride * ws % 16 == 0 && out_stride * ws % 16 == 0;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_);
+    const int64_t weights = slots * d->n * d->k * ws;
+    st = hip_status(profiled_launch(PK_LAYER_IN, product_flops(picks, 2 * d->n, d->k), 2 * weights, stream,
+                                    [&] { return launch_layer_in(P, vec, stream); }),
+                    "expert_layer");
+    if (st) return st;
+    return hip_status(profiled_launch(PK_LAYER_OUT, product_flops(picks, d->n, d->k), weights, stream,
+                                      [&] { return launch_layer_out(P, vec, stream); }),
+                      "expert_layer");
+  });
+}
+
+}  // extern "C"

@@ -1,6 +1,6 @@
 // Products of few rows with whole weight matrices (serving): C[t][j] = sum_k
 // A[t][k] B[j][k] for at most 16 MB rows t of one expert, both operands with
-// contiguous k, bf16 or 8-bit blocks.
+// contiguous k, bf16, 8-bit blocks or 8-bit integers.
 //
 // The weights are read once and bound everything, so nothing is staged: a block
 // takes 16 NB rows of B, its W waves split k between them, and a lane loads its
@@ -31,8 +31,13 @@ __device__ __forceinline__ SkinnyFrag skinny_load(const char* p, int g, int left
   return f;
 }
 
-// Op: kBytes steps: multiply(a, b, acc) adds one step's product of two fragments
-// for bf16; for blocks, scales(...) and a scaled multiply.  See the two uses.
+// Op: Acc, the accumulators' type (four floats or ints); step(...) adds one step's
+// products; finish(sums, row, first column, columns) turns a lane's four sums into
+// results.
+struct SkinnyFloat {
+  using Acc = f32x4_t;
+  __device__ __forceinline__ f32x4_t finish(const f32x4_t& v, int, int, int) const { return v; }
+};
 template <class Op, int MB, int NB, int W, typename OutT>
 __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_t lda, const char* b, int64_t ldb,
                                              OutT* c, int64_t ldc, int rows, int cols, int64_t row_bytes,
@@ -40,11 +45,12 @@ __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_
   constexpr int U = 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  f32x4_t acc[NB][MB];
+  using Acc = typename Op::Acc;
+  Acc acc[NB][MB];
 #pragma unroll
   for (int n = 0; n < NB; ++n)
 #pragma unroll
-    for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MB; ++m) acc[n][m] = Acc{0, 0, 0, 0};
   const int steps = int((row_bytes + 127) / 128);
   // rows past the end read the last one: their results are not stored
   const char* bp[NB];
@@ -80,14 +86,15 @@ __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_
   for (int n = 0; n < NB; ++n)
 #pragma unroll
     for (int m = 0; m < MB; ++m)
-      *reinterpret_cast<f32x4_t*>(sums + ((wave * NB * MB + n * MB + m) * 64 + lane) * 4) = acc[n][m];
+      *reinterpret_cast<Acc*>(sums + ((wave * NB * MB + n * MB + m) * 64 + lane) * 4) = acc[n][m];
   __syncthreads();
   for (int q = wave; q < NB * MB; q += W) {
-    f32x4_t v = *reinterpret_cast<const f32x4_t*>(sums + (q * 64 + lane) * 4);
+    Acc sum = *reinterpret_cast<const Acc*>(sums + (q * 64 + lane) * 4);
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += *reinterpret_cast<const f32x4_t*>(sums + ((w * NB * MB + q) * 64 + lane) * 4);
+    for (int w = 1; w < W; ++w) sum += *reinterpret_cast<const Acc*>(sums + ((w * NB * MB + q) * 64 + lane) * 4);
     const int n = q / MB, t = 16 * (q % MB) + r;
     if (t < rows) {
+      const f32x4_t v = op.finish(sum, t, 16 * n + 4 * g, cols);
       const float x[4] = {v[0], v[1], v[2], v[3]};
       store4<OutT>(c + t * ldc, 16 * n + 4 * g, cols, accumulate, x);
     }

@@ -1,0 +1,78 @@
+"""Oracle of the AdamW step with 8-bit states, in numpy.
+
+TEST INFRASTRUCTURE ONLY.  The formula is that of oracle.adamw; a state is held
+as e4m3 values with one fp32 scale per 128 elements (the first moment to
+nearest even, the root of the second one at random).  The states are repeated in
+fp32 operation by operation, as the header defines them, so that their bits can
+be compared; the parameter is formed in float64 from those states' inputs.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+BLOCK = 128
+F = np.float32
+# the e4m3 values that are not negative, by code
+CODES = np.array([(c & 7) * 2.0 ** -9 if c < 8 else (8 + (c & 7)) * 2.0 ** ((c >> 3) - 10) for c in range(127)])
+
+
+def values(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:
+    """fp32 values of a state (uint8 codes, fp32 scales)."""
+    mag = np.where((codes & 127) == 127, np.nan, CODES[np.minimum(codes & 127, 126)]).astype(F)
+    return np.where(codes & 128, -mag, mag) * np.repeat(scale, BLOCK)[:codes.size]
+
+
+def _scale(x: np.ndarray) -> np.ndarray:
+    pad = np.zeros(-(-x.size // BLOCK) * BLOCK, F)
+    pad[:x.size] = np.abs(x)
+    return np.maximum(pad.reshape(-1, BLOCK).max(1) / F(448), F(2.0 ** -126))
+
+
+def nearest(x: np.ndarray):
+    """(codes, scale): to nearest even."""
+    scale = _scale(x)
+    y = np.abs(x * np.repeat(F(1) / scale, BLOCK)[:x.size]).astype(np.float64)
+    hi = np.clip(np.searchsorted(CODES, y), 1, 126)
+    lo = hi - 1
+    up = (CODES[hi] - y < y - CODES[lo]) | ((CODES[hi] - y == y - CODES[lo]) & (hi % 2 == 0))
+    return (np.where(up, hi, lo) | np.where(np.signbit(x), 128, 0)).astype(np.uint8), scale
+
+
+def at_random(x: np.ndarray, u: np.ndarray):
+    """(codes, scale): up where the part cut off and u / 2^16 reach the spacing; the
+    sum is formed in fp32."""
+    scale = _scale(x)
+    y = np.minimum(x * np.repeat(F(1) / scale, BLOCK)[:x.size], F(448))
+    exp = np.where(y > 0, np.maximum(np.frexp(y)[1] - 1, -6), -6)
+    steps = np.floor(np.ldexp(y, 3 - exp) + u.astype(F) * F(2.0 ** -16))
+    return (steps + 8 * (exp + 6)).astype(np.uint8), scale
+
+
+def mix(x):
+    """The finaliser of MurmurHash3 of x + 0x9e3779b9."""
+    m = np.uint64(0xffffffff)
+    x = (np.uint64(x) + np.uint64(0x9e3779b9)) & m
+    x = ((x ^ (x >> np.uint64(16))) * np.uint64(0x85ebca6b)) & m
+    x = ((x ^ (x >> np.uint64(13))) * np.uint64(0xc2b2ae35)) & m
+    return x ^ (x >> np.uint64(16))
+
+
+def randoms(seed: int, step: int, place: int, n: int) -> np.ndarray:
+    key = mix(mix(mix(seed) + np.uint64(step)) + np.uint64(place))
+    i = np.arange(n, dtype=np.uint64)
+    w = mix(mix(key + i // np.uint64(8192)) + i // np.uint64(2) % np.uint64(4096))
+    return np.where(i % 2 == 0, w & np.uint64(0xffff), w >> np.uint64(16))
+
+
+def step(p, g, avg, avg_scale, root, root_scale, *, t, seed=0, place=0, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+         weight_decay=0.01):
+    """(p in float64 before its rounding, m and r in fp32, the new states as (codes, scale))."""
+    b1, b2 = betas
+    g32 = np.asarray(g, F)
+    m = F(b1) * values(avg, avg_scale) + F(1 - b1) * g32
+    r = values(root, root_scale)
+    r = np.sqrt(F(b2) * (r * r) + F(1 - b2) * (g32 * g32))
+    with np.errstate(divide="ignore", invalid="ignore"):
+        upd = lr * (m.astype(np.float64) / (1 - b1 ** t)) / (r.astype(np.float64) / np.sqrt(1 - b2 ** t) + eps)
+    return (np.asarray(p, np.float64) * (1 - lr * weight_decay) - upd, m, r, nearest(m),
+            at_random(r, randoms(seed, t, place, m.size)))
