@@ -538,7 +538,7 @@ int dmuon_block_matmul(const dmuon_block_product_t* d, const void* a, const floa
  * scale per 128 consecutive elements (the last block may be shorter): the
  * 1 x 128 blocks that dmuon_quantize_blocks writes and dmuon_dequantize_blocks
  * reads of the tensor's elements in rows of 128.  States start as zeros, scales too.
- * In between everything is fp32.  New scales are max(amax / 448, 2^-126); with
+ * In between everything is fp32.  New scales are max(amax * (1 / 448), 2^-126); with
  * y = x * (1 / scale), m is rounded to nearest even, and r = sqrt(v), which a
  * step moves by less than its neighbours are apart, at random:
  *   r's steps of E4M3 at y = floor(y / spacing + u / 2^16)
@@ -577,7 +577,7 @@ int dmuon_adamw_step_quantized(const dmuon_adamw_quantized_t* tensors, int32_t n
  * 8-bit integers with one fp32 scale per row: a token of activations, or an
  * output channel of a weight (n x k with its channels as rows).
  * dmuon_quantize_rows writes
- *   scale = max(amax / 127, 2^-126),  q = x * (1 / scale), rounded to nearest even
+ *   scale = max(amax * (1 / 127), 2^-126),  q = x * (1 / scale), rounded to nearest even
  * of every row in fp32.  With DMUON_ACT_SWIGLU a row of x is 2 cols long, gate then
  * up, and silu(gate) * up, in fp32, is what is quantised.  A row that holds a
  * NaN or an Inf gets a scale that is not finite and decodes to NaN; other rows
@@ -634,7 +634,8 @@ int dmuon_row_matmul(const dmuon_row_product_t* d, const void* a, const float* a
  * ids are device data that the host never reads.  An id outside 0..experts - 1 is
  * nobody's: that pick adds nothing, and a token without picks gets zeros.  A
  * token may pick an expert twice: its gates add up.  Sums are fp32; the hidden
- * activation times its gate is rounded to bf16, y is rounded once.  Results are
+ * activation times its gate is held as two bf16 values (2^-17 of it lost), y is rounded
+ * once.  Results are
  * deterministic.  A value that is not finite reaches its own token only, one of a
  * weight only the tokens of its expert.
  * workspace: dmuon_expert_layer_workspace_size bytes of device memory, 16-byte

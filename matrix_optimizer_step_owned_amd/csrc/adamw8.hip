@@ -3,7 +3,7 @@
 //   v <- beta2 v + (1 - beta2) g^2
 //   p <- p (1 - lr wd) - (lr / (1 - beta1^t)) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 // m and r = sqrt(v) are held as e4m3 values with one fp32 scale per 128
-// consecutive elements (scale = max(amax / 448, 2^-126)), the second moment by
+// consecutive elements (scale = max(amax * (1 / 448), 2^-126)), the second moment by
 // its root because its own range would be the square of what e4m3 has.
 // Between load and store everything is fp32.
 //
@@ -24,7 +24,7 @@ namespace dmuon {
 namespace {
 
 constexpr uint32_t kMinNormal = 121u << 23;      // exponent bits of e4m3's smallest normal number, 2^-6
-constexpr float kStateMax = 448.f;
+constexpr float kStateMax = 448.f, kPerMax = 1.f / 448.f;
 
 // Loads and stores of any alignment, not kept in the caches: every byte is
 // used once.
@@ -139,7 +139,7 @@ __device__ __forceinline__ float block_scale(const float (&x)[8]) {
     const uint32_t b = __float_as_uint(x[e]) & 0x7fffffffu;
     m = b > m ? b : m;
   }
-  const float s = __uint_as_float(max16(m)) / kStateMax;
+  const float s = __uint_as_float(max16(m)) * kPerMax;
   return s < 0x1p-126f ? 0x1p-126f : s;
 }
 

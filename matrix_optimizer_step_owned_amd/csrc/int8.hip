@@ -2,7 +2,7 @@
 // a weight): quantisation, its inverse, and the matrix product of such operands.
 //
 // Quantising a row:
-//   scale = max(amax / 127, 2^-126),  q = rne(x * (1 / scale))
+//   scale = max(amax * (1 / 127), 2^-126),  q = rne(x * (1 / scale))
 // in fp32, so |q| <= 127; with a gated activation x = silu(gate) * up first, in
 // fp32 too.  The maximum is taken over the bit patterns of |x|, in which NaN >
 // Inf > any number: a row with a NaN or an Inf gets a scale that is not finite
@@ -22,7 +22,7 @@ namespace {
 
 // ---- quantisation -----------------------------------------------------------
 
-constexpr float kIntMax = 127.f;
+constexpr float kPerMax = 1.f / 127.f;
 constexpr float kScaleMin = 0x1p-126f;
 constexpr int kRowThreads = 256;
 
@@ -136,7 +136,7 @@ quantize_rows_kernel(RowsArgs P) {
 #pragma unroll
       for (int w = 0; w < kRowThreads / 64; ++w) m = wave_max[w] > m ? wave_max[w] : m;
     }
-    float scale = __uint_as_float(m) / kIntMax;
+    float scale = __uint_as_float(m) * kPerMax;
     if (scale < kScaleMin) scale = kScaleMin;     // a NaN stays
     const float inv = 1.f / scale;
     if (!in) continue;                      // whole waves with T = 64, never with more

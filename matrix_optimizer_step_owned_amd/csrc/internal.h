@@ -290,7 +290,7 @@ struct LayerArgs {
   const void* w_out;         // experts x k x n
   const float* out_scale;    // experts x k, or null
   void* y;
-  uint16_t* h;               // workspace: tokens * top_k rows of n bf16
+  uint16_t* h;               // workspace: tokens * top_k rows of two parts of n bf16
   int64_t n, k, ldx, ldy, ld_in, ld_out, in_stride, out_stride;
   int32_t tokens, experts, top_k;
 };

@@ -4,8 +4,11 @@
 // with G and U the two halves of the rows of w_in[e] (2n x k), D = w_out[e] (k x n)
 // and g the token's gate of that expert.  Weights are bf16, or 8-bit integers
 // with a scale per output channel, which become bf16 in registers (exactly).
-// Sums are fp32 over v_mfma_f32_16x16x32_bf16; h is rounded to bf16 once, as
-// an operand of the second product; y is rounded once.
+// Sums are fp32 over v_mfma_f32_16x16x32_bf16.  h is an operand of the second
+// product as the sum of two bf16 values, its rounding and the rounding of what
+// that left (2^-17 of it is lost): one alone would add as much error as the
+// rounding of y (2.4e-3 in place of 1.7e-3 of y's norm), and the second costs
+// matrix instructions that the weights' loads hide.  y is rounded once.
 //
 // Every touched expert's weights are read once and bound everything.  So, as in
 // skinny.h, nothing is staged: lanes load their fragments straight into
@@ -164,8 +167,8 @@ __device__ __forceinline__ void find_rows(const LayerArgs& P, const Touched& set
   }
 }
 
-// Rows of h: whole 16-byte chunks.
-__device__ __forceinline__ int64_t pitch_of(int64_t n) { return (n + 7) / 8 * 8; }
+// Rows of h, elements: both parts one behind the other, whole 16-byte chunks.
+__device__ __forceinline__ int64_t part_of(int64_t n) { return (n + 7) / 8 * 8; }
 
 // Sixteen columns of h (16 rows of G and of U) of one expert.
 template <bool I8, bool VEC, int MB>
@@ -186,7 +189,7 @@ layer_in_kernel(LayerArgs P) {
   if (e < 0) return;
   const int r = lane & 15, g = lane >> 4;
   const int cols = int(P.n - 16 * tn < 16 ? P.n - 16 * tn : 16);
-  const int64_t bytes = P.k * (I8 ? 1 : 2), pitch = pitch_of(P.n);
+  const int64_t bytes = P.k * (I8 ? 1 : 2), part = part_of(P.n);
   const int steps = int((bytes + 127) / 128);
   // columns past the end read the last one: their results are not stored
   const int64_t j = 16 * int64_t(tn) + (r < cols ? r : cols - 1);
@@ -251,8 +254,11 @@ layer_in_kernel(LayerArgs P) {
           }
           x[q] = gated(a, b) * gate;
         }
-        uint16_t* h = P.h + (int64_t(rows.token[i]) * P.top_k + rows.pick[i]) * pitch + 16 * int64_t(tn);
+        uint16_t* h = P.h + (int64_t(rows.token[i]) * P.top_k + rows.pick[i]) * 2 * part + 16 * int64_t(tn);
         store4<uint16_t>(h, 4 * g, cols, false, x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] -= bf16_lo(pack2_bf16(x[q], 0.f));
+        store4<uint16_t>(h + part, 4 * g, cols, false, x);
       }
     }
   }
@@ -286,7 +292,7 @@ layer_out_kernel(LayerArgs P) {
   const int r = lane & 15, g = lane >> 4;
   const int64_t c0 = 16 * int64_t(blockIdx.x);
   const int cols = int(P.k - c0 < 16 ? P.k - c0 : 16);
-  const int64_t bytes = P.n * (I8 ? 1 : 2), pitch = pitch_of(P.n);
+  const int64_t bytes = P.n * (I8 ? 1 : 2), part = part_of(P.n);
   const int steps = int((bytes + 127) / 128), units = (steps + U - 1) / U;
   const int64_t j = c0 + (r < cols ? r : cols - 1);
   f32x4_t acc[MB];
@@ -307,22 +313,27 @@ layer_out_kernel(LayerArgs P) {
         for (int q = P.top_k - 1; q >= 0; --q)
           if (ids[t * P.top_k + q] == e) pick = q;
       has[m] = pick >= 0;
-      hp[m] = reinterpret_cast<const char*>(P.h + (int64_t(t) * P.top_k + (pick < 0 ? 0 : pick)) * pitch);
+      hp[m] = reinterpret_cast<const char*>(P.h + (int64_t(t) * P.top_k + (pick < 0 ? 0 : pick)) * 2 * part);
     }
     WeightStep w[U];
-    RowStep<I8> x[U][MB];
+    RowStep<I8> x[U][2][MB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t at = int64_t(s0 + u) * 128;
       w[u] = load_weight<I8, VEC>(wp, at, bytes, g);
 #pragma unroll
-      for (int m = 0; m < MB; ++m) x[u][m] = load_row<I8, VEC>(hp[m], at, has[m] ? bytes : 0, g);
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+          x[u][q][m] = load_row<I8, VEC>(hp[m] + q * part * 2, at, has[m] ? bytes : 0, g);
     }
     f32x4_t p[MB];
 #pragma unroll
     for (int m = 0; m < MB; ++m) p[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < U; ++u) add_step<I8, MB>(w[u], x[u], p);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) add_step<I8, MB>(w[u], x[u][q], p);
     // only the expert's own tokens: a weight that is not finite is nobody else's
 #pragma unroll
     for (int q = 0; q < 4; ++q) {

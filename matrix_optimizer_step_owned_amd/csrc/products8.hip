@@ -272,7 +272,7 @@ size_t dmuon_expert_layer_workspace_size(const dmuon_expert_layer_t* d) {
   if (!d || d->tokens < 1 || d->tokens > kLayerTokens || d->top_k < 1 || d->top_k > kLayerPicks || d->n < 1 ||
       d->n > kMaxDim)
     return 0;
-  return static_cast<size_t>(d->tokens * d->top_k * up(d->n, 8) * 16);
+  return static_cast<size_t>(d->tokens * d->top_k * up(d->n, 8) * 32);
 }
 
 int dmuon_expert_layer(const dmuon_expert_layer_t* d, const void* x, const int32_t* ids, const float* gates,

@@ -25,7 +25,7 @@ def values(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:
 def _scale(x: np.ndarray) -> np.ndarray:
     pad = np.zeros(-(-x.size // BLOCK) * BLOCK, F)
     pad[:x.size] = np.abs(x)
-    return np.maximum(pad.reshape(-1, BLOCK).max(1) / F(448), F(2.0 ** -126))
+    return np.maximum(pad.reshape(-1, BLOCK).max(1) * (F(1) / F(448)), F(2.0 ** -126))
 
 
 def nearest(x: np.ndarray):

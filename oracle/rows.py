@@ -13,7 +13,7 @@ F = np.float32
 def quantize(x):
     """(q, scale) of fp32 rows."""
     x = np.asarray(x, F)
-    scale = np.maximum(np.abs(x).max(-1) / F(127), F(2.0 ** -126))
+    scale = np.maximum(np.abs(x).max(-1) * (F(1) / F(127)), F(2.0 ** -126))
     return np.rint(x * (F(1) / scale)[..., None]).astype(np.int8), scale
 
 
@@ -43,8 +43,8 @@ def layer(x, ids, gates, w_in, w_out):
     """(y, the fp32 error's and the rounding's bound without y's own rounding) of a layer of
     experts; float64 weights.  A sum of len products in fp32 is off by (len + 8) 2^-24 of
     the sum of their magnitudes (operands, products, scale); silu in fp32 by
-    (2 |a| + 16) 2^-23 of itself, and moves by at most 1.1 of its argument's error; h is rounded to
-    bf16, half a step of 2^-8."""
+    (2 |a| + 16) 2^-23 of itself, and moves by at most 1.1 of its argument's error; h is held as two
+    bf16 values, each off by half a step: 2^-16 of it."""
     tokens, top_k = ids.shape
     n, k = w_out.shape[2], w_out.shape[1]
     y, err, mag = np.zeros((tokens, k)), np.zeros((tokens, k)), np.zeros((tokens, k))
@@ -56,8 +56,8 @@ def layer(x, ids, gates, w_in, w_out):
             da, db = ((k + 8) * u * (np.abs(w) @ np.abs(x[t])) for w in (w_in[e][:n], w_in[e][n:]))
             h = gate * silu(a) * b
             dh = np.abs(gate) * (1.1 * da * (np.abs(b) + db) + np.abs(silu(a)) * db) + np.abs(h) * (2 * np.abs(a) + 16) * 2 * u
-            dh += 2.0 ** -8 * (np.abs(h) + dh) + 2.0 ** -133
+            dh += 2.0 ** -16 * (np.abs(h) + dh) + 2.0 ** -133
             y[t] += w_out[e] @ h
             err[t] += np.abs(w_out[e]) @ dh
             mag[t] += np.abs(w_out[e]) @ (np.abs(h) + dh)
-    return y, err + (n * top_k + 8) * u * mag
+    return y, err + (2 * n * top_k + 8) * u * mag

@@ -136,7 +136,7 @@ def test_layer_refusals(dm):
         return dm._lib.dmuon_expert_layer(d, x, ids, gates, w_in, si, w_out, so, y, ws, wsb, None)
 
     need = dm._lib.dmuon_expert_layer_workspace_size
-    assert need(layer()) == 10 * 2 * 48 * 2 and need(layer(n=45)) == need(layer())
+    assert need(layer()) == 10 * 2 * 48 * 4 and need(layer(n=45)) == need(layer())
     assert need(None) == 0 and need(layer(tokens=0)) == 0 and need(layer(tokens=65)) == 0
     assert call(None) == bad
     for kw in (dict(tokens=-1), dict(tokens=65), dict(n=0), dict(k=0), dict(experts=0), dict(experts=4097), dict(top_k=0),
@@ -152,7 +152,7 @@ def test_layer_refusals(dm):
     assert call(layer(weight_dtype=4), si=si) == bad
     assert call(layer(weight_dtype=4), si=si, so=so + 2) == bad
     assert call(layer(), ws=None) == dm.DMUON_ERR_WORKSPACE
-    assert call(layer(), wsb=10 * 2 * 48 * 2 - 1) == dm.DMUON_ERR_WORKSPACE
+    assert call(layer(), wsb=10 * 2 * 48 * 4 - 1) == dm.DMUON_ERR_WORKSPACE
     for kw in (dict(y=x), dict(y=ids), dict(y=w_in + 2 * 96 * 64 * 7), dict(ws=w_out), dict(ws=y), dict(ws=gates)):
         assert call(layer(), **kw) == dm.DMUON_ERR_ALIASING, kw
     assert call(layer(weight_dtype=4), si=si, so=y) == dm.DMUON_ERR_ALIASING
