@@ -168,6 +168,17 @@ __device__ __forceinline__ float gated(float gate, float up) {
   return gate * __builtin_amdgcn_rcpf(1.f + __expf(-gate)) * up;
 }
 
+// Scales of four consecutive columns of `cols`.
+__device__ __forceinline__ f32x4_t four_scales(const float* s, int col, int cols) {
+  struct __attribute__((packed, aligned(4))) Any { f32x4_t v; };
+  if (col + 4 <= cols) return reinterpret_cast<const Any*>(s + col)->v;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < cols) v[e] = s[col + e];
+  return v;
+}
+
 // Sixteen bytes from p, of which the first `valid` elements of EB bytes are
 // inside the row; the others read as zero.  VEC: p is 16-byte aligned and
 // `valid` is either <= 0 or a whole chunk.  Without VEC a chunk that ends
@@ -195,6 +206,16 @@ __device__ __forceinline__ u32x4_t load_chunk(const char* p, int valid) {
     }
   }
   return v;
+}
+
+// Sixteen bytes without the first `gone` (1 and more): the others move down, zeros follow.
+__device__ __forceinline__ u32x4_t moved_down(const u32x4_t& w, int gone) {
+  const uint64_t lo = (uint64_t(w[1]) << 32) | w[0], hi = (uint64_t(w[3]) << 32) | w[2];
+  const int bits = 8 * gone;
+  uint64_t l = bits < 64 ? (lo >> bits) | (hi << (64 - bits)) : hi >> (bits & 63);
+  uint64_t h = bits < 64 ? hi >> bits : 0;
+  if (bits >= 128) l = 0;
+  return u32x4_t{uint32_t(l), uint32_t(l >> 32), uint32_t(h), uint32_t(h >> 32)};
 }
 
 // Buffer descriptor of `bytes` bytes at `base` (raw buffer, no stride), in

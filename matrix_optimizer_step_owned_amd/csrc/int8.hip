@@ -234,16 +234,6 @@ __device__ __forceinline__ i32x4_t multiply(const u32x4_t& b, const u32x4_t& a, 
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, b), __builtin_bit_cast(i32x4_t, a), c, 0, 0, 0);
 }
 
-// Scales of four consecutive columns of `cols`.
-__device__ __forceinline__ f32x4_t four_scales(const float* s, int col, int cols) {
-  struct __attribute__((packed, aligned(4))) Any { f32x4_t v; };
-  if (col + 4 <= cols) return reinterpret_cast<const Any*>(s + col)->v;
-  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (col + e < cols) v[e] = s[col + e];
-  return v;
-}
 __device__ __forceinline__ f32x4_t scaled(const i32x4_t& sum, float sa, const f32x4_t& sb) {
   return f32x4_t{float(sum[0]) * sa * sb[0], float(sum[1]) * sa * sb[1], float(sum[2]) * sa * sb[2],
                  float(sum[3]) * sa * sb[3]};

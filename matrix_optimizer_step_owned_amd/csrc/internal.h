@@ -290,10 +290,11 @@ struct LayerArgs {
   const void* w_out;         // experts x k x n
   const float* out_scale;    // experts x k, or null
   void* y;
-  uint16_t* h;               // workspace: tokens * top_k rows of two parts of n bf16
+  void* workspace;           // 16-byte aligned, layer_workspace() bytes
   int64_t n, k, ldx, ldy, ld_in, ld_out, in_stride, out_stride;
   int32_t tokens, experts, top_k;
 };
+int64_t layer_workspace(const LayerArgs& P);     // of its sizes
 hipError_t launch_layer_in(const LayerArgs& P, bool vec, hipStream_t stream);
 hipError_t launch_layer_out(const LayerArgs& P, bool vec, hipStream_t stream);
 

@@ -12,12 +12,14 @@
 //
 // Every touched expert's weights are read once and bound everything.  So, as in
 // skinny.h, nothing is staged: lanes load their fragments straight into
-// registers, 32 of the 128 bytes that a row has in one step, waves split the
-// sum and add up in LDS in wave order.  Which experts are touched is device
-// data: layer_in has blocks for as many experts as there can be and each finds
-// its own from the ids.  In layer_out a block keeps its 16 output columns for
-// all tokens and runs over the touched experts, so that no sum crosses blocks: a
-// token that did not pick the expert has zeros in place of h.
+// registers, 32 of the 128 bytes that a row has in one step.  Which experts are
+// touched is device data: layer_in has blocks for as many experts as there can
+// be and each finds its own from the ids.  One block more lists the touched
+// experts and their rows for layer_out, where every wave runs over a part of
+// (expert, steps of its rows) for 16 output columns and adds the rows' sums to
+// the tokens' in LDS; waves, and blocks that split the same columns, add up
+// in a fixed order, so results do not depend on the order of execution.
+#include "bigtile.h"
 #include "skinny.h"
 
 namespace dmuon {
@@ -25,12 +27,6 @@ namespace {
 
 constexpr int kLayerWaves = 8;
 constexpr int kLayerThreads = kLayerWaves * 64;
-
-// Sixteen bytes of a row at p, of which `left` bytes are inside; elements of EB bytes.
-template <int EB, bool VEC>
-__device__ __forceinline__ u32x4_t chunk_of(const char* p, int64_t left) {
-  return load_chunk<EB, VEC>(p, left < 0 ? 0 : left > 16 ? 16 / EB : int(left) / EB);
-}
 
 __device__ __forceinline__ f32x4_t multiply(const bf16x8_t& b, const bf16x8_t& a, const f32x4_t& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
@@ -52,44 +48,71 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// Rows of any alignment and length are read in one of three ways.  kWhole: aligned,
+// a multiple of 16 bytes.  kMoved: at least 16 bytes long.  Both read a chunk that
+// ends past the row from further down, where the row ends, and put it right before it is
+// used (trim).  kSingle: shorter, element by element.
+enum RowMode { kWhole, kMoved, kSingle };
+
+template <int EB, RowMode MODE>
+__device__ __forceinline__ u32x4_t row_chunk(const char* row, int at, int bytes) {
+  if constexpr (MODE == kSingle) {
+    const int left = (bytes - at) / EB;
+    return load_chunk<EB, false>(row + at, left < 0 ? 0 : left > 16 / EB ? 16 / EB : left);
+  } else {
+    struct __attribute__((packed, aligned(MODE == kWhole ? 16 : EB))) Any { u32x4_t v; };
+    return reinterpret_cast<const Any*>(row + (at < bytes - 16 ? at : bytes - 16))->v;
+  }
+}
+template <RowMode MODE>
+__device__ __forceinline__ void trim_chunk(u32x4_t& v, int at, int bytes) {
+  const int gone = at - (bytes - 16);
+  if constexpr (MODE == kWhole) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = gone > 0 ? 0u : v[i];
+  } else if constexpr (MODE == kMoved) {
+    if (gone > 0) v = moved_down(v, gone);
+  }
+}
+
 // One step (128 bytes of a weight row) of the weights and of the rows that they
-// multiply: a bf16 row has 128 bytes of it, or 256 with 8-bit weights.
+// multiply: a bf16 row has 128 bytes of it, or 256 with 8-bit weights.  `at`,
+// `bytes`: of the weight row.
+template <bool I8, RowMode MODE>
 struct WeightStep {
   u32x4_t h[2];
-};
-template <bool I8>
-struct RowStep {
-  u32x4_t h[I8 ? 4 : 2];
-};
-template <bool I8, bool VEC>
-__device__ __forceinline__ WeightStep load_weight(const char* row, int64_t at, int64_t bytes, int g) {
-  WeightStep w;
+  __device__ __forceinline__ void load(const char* row, int at, int bytes, int g) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t o = at + 64 * h + 16 * g;
-    w.h[h] = chunk_of<I8 ? 1 : 2, VEC>(row + o, bytes - o);
+    for (int i = 0; i < 2; ++i) h[i] = row_chunk<I8 ? 1 : 2, MODE>(row, at + 64 * i + 16 * g, bytes);
   }
-  return w;
-}
-// `at`, `bytes`: of the weight row.
-template <bool I8, bool VEC>
-__device__ __forceinline__ RowStep<I8> load_row(const char* row, int64_t at, int64_t bytes, int g) {
-  RowStep<I8> x;
+  __device__ __forceinline__ void trim(int at, int bytes, int g) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t o = at + 64 * h + 16 * g;
-    if constexpr (I8) {
-      x.h[2 * h] = chunk_of<2, VEC>(row + 2 * o, 2 * (bytes - o));
-      x.h[2 * h + 1] = chunk_of<2, VEC>(row + 2 * o + 16, 2 * (bytes - o) - 16);
-    } else {
-      x.h[h] = chunk_of<2, VEC>(row + o, bytes - o);
+    for (int i = 0; i < 2; ++i) trim_chunk<MODE>(h[i], at + 64 * i + 16 * g, bytes);
+  }
+};
+template <bool I8, RowMode MODE>
+struct RowStep {
+  static constexpr int N = I8 ? 4 : 2;
+  u32x4_t h[N];
+  static __device__ __forceinline__ int offset(int i, int at, int g) {
+    return I8 ? 2 * (at + 64 * (i >> 1) + 16 * g) + 16 * (i & 1) : at + 64 * i + 16 * g;
+  }
+  __device__ __forceinline__ void load(const char* row, int at, int bytes, int g) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = row_chunk<2, MODE>(row, offset(i, at, g), I8 ? 2 * bytes : bytes);
+  }
+  // With kWhole the weights' zeros are enough: what is read in their place is the row's own.
+  __device__ __forceinline__ void trim(int at, int bytes, int g) {
+    if constexpr (MODE == kMoved) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) trim_chunk<MODE>(h[i], offset(i, at, g), I8 ? 2 * bytes : bytes);
     }
   }
-  return x;
-}
+};
 // acc[m] += one step's products with MB blocks of rows; the weights are widened once.
-template <bool I8, int MB>
-__device__ __forceinline__ void add_step(const WeightStep& w, const RowStep<I8> (&x)[MB], f32x4_t (&acc)[MB]) {
+template <bool I8, RowMode MODE, int MB>
+__device__ __forceinline__ void add_step(const WeightStep<I8, MODE>& w, const RowStep<I8, MODE> (&x)[MB],
+                                         f32x4_t (&acc)[MB]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if constexpr (I8) {
@@ -107,95 +130,200 @@ __device__ __forceinline__ void add_step(const WeightStep& w, const RowStep<I8> 
   }
 }
 
-// Set of the touched experts: one bit each.  Ids outside 0 .. experts - 1 are
-// nobody's.  All threads of the block call it; a barrier behind it is the caller's.
-struct Touched {
-  uint32_t bits[kLayerExperts / 32];
-  __device__ __forceinline__ void build(const LayerArgs& P) {
-    for (int i = threadIdx.x; i < kLayerExperts / 32; i += kLayerThreads) bits[i] = 0;
-    __syncthreads();
+// The ids of a call in LDS, -1 for nobody's.
+struct Ids {
+  int16_t of[kLayerTokens * kLayerPicks];
+  __device__ __forceinline__ void load(const LayerArgs& P) {
     for (int i = threadIdx.x; i < P.tokens * P.top_k; i += kLayerThreads) {
       const uint32_t id = uint32_t(P.ids[i]);
-      if (id < uint32_t(P.experts)) atomicOr(&bits[id >> 5], 1u << (id & 31));
+      of[i] = id < uint32_t(P.experts) ? int16_t(id) : int16_t(-1);
     }
+  }
+  // The first pick of expert e by token t, -1 if there is none.
+  __device__ __forceinline__ int pick(const LayerArgs& P, int t, int e) const {
+    int pick = -1;
+    for (int j = P.top_k - 1; j >= 0; --j)
+      if (of[t * P.top_k + j] == e) pick = j;
+    return pick;
   }
 };
 
 // The rows of one expert: the tokens that picked it, in their order.
 struct ExpertRows {
-  int expert, count;         // -1: no such expert
+  uint32_t bits[kLayerExperts / 32];      // set of the touched experts
+  int expert, count;                      // -1: no such expert
   int token[kLayerTokens], pick[kLayerTokens];
   float gate[kLayerTokens];
-};
 
-// The slot-th touched expert and its rows, found by one wave.  A token that
-// picked an expert twice has one row, with the sum of its gates.
-__device__ __forceinline__ void find_rows(const LayerArgs& P, const Touched& set, int slot, ExpertRows* out) {
-  static_assert(kLayerExperts / 32 <= 128 && kLayerTokens <= 64, "two words and one token per lane");
-  const int lane = threadIdx.x & 63;
-  const uint32_t a = set.bits[2 * lane], b = set.bits[2 * lane + 1];
-  const int n = __popc(a) + __popc(b), upto = wave_scan_sum(n);
-  const uint64_t hit = __ballot(upto > slot);
-  int expert = -1;
-  if (hit) {
-    const int l = __builtin_ctzll(hit);
-    int left = slot - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
-    uint64_t word = (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(b), l))) << 32) |
-                    uint32_t(__builtin_amdgcn_readlane(int(a), l));
-    for (; left > 0; --left) word &= word - 1;
-    expert = 64 * l + __builtin_ctzll(word);
+  __device__ __forceinline__ void clear() {
+    for (int i = threadIdx.x; i < kLayerExperts / 32; i += kLayerThreads) bits[i] = 0;
   }
-  int pick = -1;
-  float gate = 0.f;
-  if (lane < P.tokens && expert >= 0) {
-    for (int j = 0; j < P.top_k; ++j) {
-      if (P.ids[lane * P.top_k + j] != expert) continue;
-      if (pick < 0) pick = j;
-      gate += P.gates[lane * P.top_k + j];
+  __device__ __forceinline__ void mark(const LayerArgs& P, const Ids& ids) {
+    for (int i = threadIdx.x; i < P.tokens * P.top_k; i += kLayerThreads)
+      if (ids.of[i] >= 0) atomicOr(&bits[ids.of[i] >> 5], 1u << (ids.of[i] & 31));
+  }
+  // The slot-th touched expert and its rows, by one wave.  A token that picked
+  // an expert twice has one row, with the sum of its gates.
+  __device__ __forceinline__ void find(const LayerArgs& P, const Ids& ids, int slot) {
+    static_assert(kLayerExperts / 32 <= 128 && kLayerTokens <= 64, "two words and one token per lane");
+    const int lane = threadIdx.x & 63;
+    const uint32_t a = bits[2 * lane], b = bits[2 * lane + 1];
+    const int n = __popc(a) + __popc(b), upto = wave_scan_sum(n);
+    const uint64_t hit = __ballot(upto > slot);
+    int e = -1;
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      int left = slot - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
+      uint64_t word = (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(b), l))) << 32) |
+                      uint32_t(__builtin_amdgcn_readlane(int(a), l));
+      for (; left > 0; --left) word &= word - 1;
+      e = 64 * l + __builtin_ctzll(word);
+    }
+    const int first = lane < P.tokens && e >= 0 ? ids.pick(P, lane, e) : -1;
+    const uint64_t rows = __ballot(first >= 0);
+    if (first >= 0) {
+      float g = 0.f;
+      for (int j = first; j < P.top_k; ++j)
+        if (ids.of[lane * P.top_k + j] == e) g += P.gates[lane * P.top_k + j];
+      const int i = __popcll(rows & ((uint64_t(1) << lane) - 1));
+      token[i] = lane;
+      pick[i] = first;
+      gate[i] = g;
+    }
+    if (lane == 0) {
+      expert = e;
+      count = __popcll(rows);
     }
   }
-  const uint64_t rows = __ballot(pick >= 0);
-  if (pick >= 0) {
-    const int i = __popcll(rows & ((uint64_t(1) << lane) - 1));
-    out->token[i] = lane;
-    out->pick[i] = pick;
-    out->gate[i] = gate;
-  }
-  if (lane == 0) {
-    out->expert = expert;
-    out->count = __popcll(rows);
-  }
+};
+
+// What layer_out reads of the routing: the touched experts, and for the s-th of
+// them rows first[s] .. first[s + 1] - 1, each a token and its first pick of that expert.
+struct Routing {
+  int slots;
+  uint16_t expert[kLayerExperts], first[kLayerExperts + 1];
+  uint16_t rows[kLayerTokens * kLayerPicks];     // 64 token + pick
+};
+// The workspace: h, rows of two parts of n bf16; the routing; a count of arrived
+// blocks per 16 columns of y; sums of blocks that split the same columns.
+struct Space {
+  uint16_t* h;
+  Routing* routing;
+  int32_t* arrived;
+  float* sums;
+};
+__host__ __device__ inline int64_t part_of(int64_t n) { return (n + 7) / 8 * 8; }
+__host__ __device__ inline int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+__host__ __device__ inline Space space_of(const LayerArgs& P) {
+  Space s;
+  char* p = static_cast<char*>(P.workspace);
+  s.h = reinterpret_cast<uint16_t*>(p);
+  p += whole(int64_t(P.tokens) * P.top_k * 4 * part_of(P.n));
+  s.routing = reinterpret_cast<Routing*>(p);
+  p += whole(sizeof(Routing));
+  s.arrived = reinterpret_cast<int32_t*>(p);
+  p += whole((P.k + 15) / 16 * 4);
+  s.sums = reinterpret_cast<float*>(p);
+  return s;
 }
 
-// Rows of h, elements: both parts one behind the other, whole 16-byte chunks.
-__device__ __forceinline__ int64_t part_of(int64_t n) { return (n + 7) / 8 * 8; }
-
-// Sixteen columns of h (16 rows of G and of U) of one expert.
-template <bool I8, bool VEC, int MB>
-__global__ void __launch_bounds__(kLayerThreads)
-layer_in_kernel(LayerArgs P) {
-  constexpr int U = I8 ? 2 : 4;
-  __shared__ Touched set;
-  __shared__ ExpertRows rows;
-  __shared__ __attribute__((aligned(16))) float sums[kLayerWaves * 2 * MB * 256];
-  const uint32_t nt = (uint32_t(P.n) + 15) / 16;
-  const int slot = int(blockIdx.x / nt), tn = int(blockIdx.x - uint32_t(slot) * nt);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  set.build(P);
+// One block lists the touched experts and their rows.  Which of an expert's rows
+// comes first may differ from run to run; no sum depends on it.
+struct RoutingScratch {
+  int count[kLayerExperts];
+  int waves[2 * kLayerWaves];
+};
+__device__ __forceinline__ void list_rows(const LayerArgs& P, const Ids& ids, RoutingScratch& S, const Space& W) {
+  constexpr int PER = kLayerExperts / kLayerThreads;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, picks = P.tokens * P.top_k;
+  for (int64_t i = t; i < (P.k + 15) / 16; i += kLayerThreads) W.arrived[i] = 0;
+  for (int i = t; i < kLayerExperts; i += kLayerThreads) S.count[i] = 0;
   __syncthreads();
-  if (wave == 0) find_rows(P, set, slot, &rows);
+  auto is_first = [&](int i) { return ids.of[i] >= 0 && ids.pick(P, i / P.top_k, ids.of[i]) == i % P.top_k; };
+  for (int i = t; i < picks; i += kLayerThreads)
+    if (is_first(i)) atomicAdd(&S.count[ids.of[i]], 1);
+  __syncthreads();
+  // thread t has experts PER t .. PER t + PER - 1: running counts of touched ones and of rows
+  int own[PER], touched = 0, rows = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    own[i] = S.count[PER * t + i];
+    touched += own[i] > 0;
+    rows += own[i];
+  }
+  int slot = wave_scan_sum(touched), first = wave_scan_sum(rows);
+  if (lane == 63) {
+    S.waves[wave] = slot;
+    S.waves[kLayerWaves + wave] = first;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    slot += S.waves[w];
+    first += S.waves[kLayerWaves + w];
+  }
+  if (t == kLayerThreads - 1) {
+    W.routing->slots = slot;
+    W.routing->first[slot] = uint16_t(first);
+  }
+  slot -= touched;
+  first -= rows;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (own[i] > 0) {
+      W.routing->expert[slot] = uint16_t(PER * t + i);
+      W.routing->first[slot] = uint16_t(first);
+      ++slot;
+    }
+    S.count[PER * t + i] = first;      // where the expert's next row goes
+    first += own[i];
+  }
+  __syncthreads();
+  for (int i = t; i < picks; i += kLayerThreads)
+    if (is_first(i)) W.routing->rows[atomicAdd(&S.count[ids.of[i]], 1)] = uint16_t(i / P.top_k * 64 + i % P.top_k);
+}
+
+// Tiles of sixteen columns of h (16 rows of G and of U) of one expert, `tiles` of them per
+// block.  `share` waves split the sum of a tile: one where there are tiles for all
+// waves, which then neither wait nor add up (32 tokens, 8 of 128 experts of 1024 x
+// 2048 in 8 bits: 137 us with eight, SHAREUS with one); otherwise they add up in LDS in
+// wave order, one wave for all, another for each round, while the others go on.
+template <bool I8, RowMode MODE, int MB>
+__global__ void __launch_bounds__(kLayerThreads, MB == 1 ? 4 : 2)
+layer_in_kernel(LayerArgs P, int groups, int tiles, int share) {
+  constexpr int U = 2, W = kLayerWaves;
+  __shared__ Ids ids;
+  union Scratch {
+    ExpertRows rows;
+    RoutingScratch list;
+  };
+  __shared__ Scratch shared;
+  __shared__ __attribute__((aligned(16))) float sums[2][W * 2 * MB * 256];
+  const int slot = int(blockIdx.x) / groups, group = int(blockIdx.x) - slot * groups;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Space space = space_of(P);
+  ids.load(P);
+  if (blockIdx.x == gridDim.x - 1) {
+    __syncthreads();
+    list_rows(P, ids, shared.list, space);
+    return;
+  }
+  ExpertRows& rows = shared.rows;
+  rows.clear();
+  __syncthreads();
+  rows.mark(P, ids);
+  __syncthreads();
+  if (wave == 0) rows.find(P, ids, slot);
   __syncthreads();
   const int e = __builtin_amdgcn_readfirstlane(rows.expert), count = __builtin_amdgcn_readfirstlane(rows.count);
   if (e < 0) return;
   const int r = lane & 15, g = lane >> 4;
-  const int cols = int(P.n - 16 * tn < 16 ? P.n - 16 * tn : 16);
-  const int64_t bytes = P.k * (I8 ? 1 : 2), part = part_of(P.n);
-  const int steps = int((bytes + 127) / 128);
-  // columns past the end read the last one: their results are not stored
-  const int64_t j = 16 * int64_t(tn) + (r < cols ? r : cols - 1);
-  const char* wp[2];
-  wp[0] = static_cast<const char*>(P.w_in) + (e * P.in_stride + j * P.ld_in) * (I8 ? 1 : 2);
-  wp[1] = wp[0] + P.n * P.ld_in * (I8 ? 1 : 2);
+  const int bytes = int(P.k) * (I8 ? 1 : 2), steps = (bytes + 127) / 128;
+  const int64_t part = part_of(P.n), row_bytes = P.ld_in * (I8 ? 1 : 2);
+  const char* const weights = static_cast<const char*>(P.w_in) + e * P.in_stride * (I8 ? 1 : 2);
+  const int last = int((P.n + 15) / 16), t0 = group * tiles, t1 = t0 + tiles < last ? t0 + tiles : last;
+  // every `at_once` tiles are a round; wave k of a tile's begins at its k-th piece
+  const int at_once = W / share, mine = wave / share, k = wave - mine * share;
+  int turn = 0;
   for (int r0 = 0; r0 < count; r0 += 16 * MB) {
     const char* xp[MB];
 #pragma unroll
@@ -203,189 +331,295 @@ layer_in_kernel(LayerArgs P) {
       const int i = r0 + 16 * m + r;
       xp[m] = static_cast<const char*>(P.x) + rows.token[i < count ? i : count - 1] * P.ldx * 2;
     }
+    WeightStep<I8, MODE> w[U][2];
+    RowStep<I8, MODE> x[U][MB];
     f32x4_t acc[2][MB];
+    // the loads of a piece (tile, step) go out before the sums of the piece before
+    // are dealt with
+    int tn = t0 + mine, s0 = k * U;
+    bool loaded = false, more = tn < t1;
+    const int first_turn = turn, turns = (t1 - t0 + at_once - 1) / at_once;
+    while (true) {
+      const int now = tn;
+      bool done = false;
+      if (!more) {
+        done = true;          // of no tile in this round, the last one
+      } else if (loaded) {
+        if ((s0 + U) * 128 > bytes) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+          for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int s0 = wave * U; s0 < steps; s0 += kLayerWaves * U) {
-      WeightStep w[U][2];
-      RowStep<I8> x[U][MB];
+            for (int n = 0; n < 2; ++n) w[u][n].trim((s0 + u) * 128, bytes, g);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t at = int64_t(s0 + u) * 128;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) w[u][n] = load_weight<I8, VEC>(wp[n], at, bytes, g);
-#pragma unroll
-        for (int m = 0; m < MB; ++m) x[u][m] = load_row<I8, VEC>(xp[m], at, bytes, g);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) add_step<I8, MB>(w[u][n], x[u], acc[n]);
-    }
-    if (r0 > 0) __syncthreads();      // the sums of the rows before are read
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int m = 0; m < MB; ++m)
-        *reinterpret_cast<f32x4_t*>(sums + ((wave * 2 * MB + n * MB + m) * 64 + lane) * 4) = acc[n][m];
-    __syncthreads();
-    if (wave < MB) {
-      f32x4_t v[2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        v[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kLayerWaves; ++w)
-          v[n] += *reinterpret_cast<const f32x4_t*>(sums + ((w * 2 * MB + n * MB + wave) * 64 + lane) * 4);
-      }
-      const int i = r0 + 16 * wave + r;
-      if (i < count) {
-        const float gate = rows.gate[i];
-        float x[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float a = v[0][q], b = v[1][q];
-          if constexpr (I8) {
-            const int64_t c = 16 * int64_t(tn) + (4 * g + q < cols ? 4 * g + q : cols - 1);
-            a *= P.in_scale[e * 2 * P.n + c];
-            b *= P.in_scale[e * 2 * P.n + P.n + c];
+            for (int m = 0; m < MB; ++m) x[u][m].trim((s0 + u) * 128, bytes, g);
           }
-          x[q] = gated(a, b) * gate;
         }
-        uint16_t* h = P.h + (int64_t(rows.token[i]) * P.top_k + rows.pick[i]) * 2 * part + 16 * int64_t(tn);
-        store4<uint16_t>(h, 4 * g, cols, false, x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] -= bf16_lo(pack2_bf16(x[q], 0.f));
-        store4<uint16_t>(h + part, 4 * g, cols, false, x);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            add_step<I8, MODE, MB>(w[u][n], x[u], acc[n]);
+            if constexpr (I8) __builtin_amdgcn_sched_barrier(0);    // one widened step at a time
+          }
+        s0 += share * U;
+        if (s0 >= steps) {
+          s0 = k * U;
+          done = true;
+          tn += at_once;
+          more = tn < t1;
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
+      loaded = true;
+      if (more) {
+        const int lane = here(int(threadIdx.x) & 63), r = lane & 15, g = lane >> 4;
+        // columns past the end read the last one: their results are not stored
+        int64_t j = 16 * int64_t(tn) + r;
+        j = j < P.n ? j : P.n - 1;
+        const char* wp = weights + j * row_bytes;
+        const char* up = wp + P.n * row_bytes;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          w[u][0].load(wp, (s0 + u) * 128, bytes, g);
+          w[u][1].load(up, (s0 + u) * 128, bytes, g);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int m = 0; m < MB; ++m) x[u][m].load(xp[m], (s0 + u) * 128, bytes, g);
+      }
+      if (!done) continue;
+      const int cols = int(P.n - 16 * now < 16 ? P.n - 16 * now : 16);
+      // h of sixteen rows from a lane's sums of them
+      auto write = [&](int m, f32x4_t a, f32x4_t b, int tile, int cols) {
+        const int i = r0 + 16 * m + r;
+        if (i >= count) return;
+        const float gate = rows.gate[i];
+        if constexpr (I8) {
+          const float* scale = P.in_scale + e * 2 * P.n + 16 * int64_t(tile);
+          a *= four_scales(scale, 4 * g, cols);
+          b *= four_scales(scale + P.n, 4 * g, cols);
+        }
+        float y[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = gated(a[q], b[q]) * gate;
+        uint16_t* h = space.h + (int64_t(rows.token[i]) * P.top_k + rows.pick[i]) * 2 * part + 16 * int64_t(tile);
+        store4<uint16_t>(h, 4 * g, cols, false, y);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] -= bf16_lo(pack2_bf16(y[q], 0.f));
+        store4<uint16_t>(h + part, 4 * g, cols, false, y);
+      };
+      if (share == 1) {
+        if (now < t1) {
+#pragma unroll
+          for (int m = 0; m < MB; ++m) write(m, acc[0][m], acc[1][m], now, cols);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      } else {
+        float* buf = sums[turn & 1];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int m = 0; m < MB; ++m) {
+            *reinterpret_cast<f32x4_t*>(buf + ((wave * 2 * MB + n * MB + m) * 64 + lane) * 4) = acc[n][m];
+            acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          }
+        wait_lds();
+        plain_barrier();
+        if (now < t1) {
+          for (int m = 0; m < MB; ++m) {
+            if (k != (turn * MB + m) % share) continue;
+            f32x4_t v[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              v[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+              for (int q = mine * share; q < (mine + 1) * share; ++q)
+                v[n] += *reinterpret_cast<const f32x4_t*>(buf + ((q * 2 * MB + n * MB + m) * 64 + lane) * 4);
+            }
+            write(m, v[0], v[1], now, cols);
+          }
+        }
+      }
+      if (++turn == first_turn + turns) break;
     }
   }
 }
 
-// Sixteen columns of y for all tokens.  The waves take (expert, four steps of
-// its rows) in turn.
-template <bool I8, bool VEC, int MB>
-__global__ void __launch_bounds__(kLayerThreads)
-layer_out_kernel(LayerArgs P) {
-  constexpr int U = I8 ? 2 : 4;
-  __shared__ Touched set;
-  __shared__ uint16_t experts[kLayerExperts];
-  __shared__ int total;
-  __shared__ int16_t ids[kLayerTokens * kLayerPicks];
-  __shared__ __attribute__((aligned(16))) float sums[kLayerWaves * MB * 256];
+// Sixteen columns of y for all tokens, or one of `splits` parts of their sums.  The
+// sums run over units: U steps of an expert's rows.  Every wave has a run of
+// them and keeps 16 rows' sums in registers while the expert stays the same.
+template <bool I8, RowMode MODE>
+__global__ void __launch_bounds__(kLayerThreads, 4)
+layer_out_kernel(LayerArgs P, int splits) {
+  constexpr int U = (I8 ? 2 : 4) / (MODE == kWhole ? 1 : 2), W = kLayerWaves;
+  __shared__ uint16_t experts[kLayerExperts], first[kLayerExperts + 1];
+  __shared__ uint16_t list[kLayerTokens * kLayerPicks];
+  __shared__ __attribute__((aligned(16))) float sums[W][kLayerTokens * 16];
+  __shared__ int last_one;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  set.build(P);
-  for (int i = threadIdx.x; i < P.tokens * P.top_k; i += kLayerThreads) {
-    const uint32_t id = uint32_t(P.ids[i]);
-    ids[i] = id < uint32_t(P.experts) ? int16_t(id) : int16_t(-1);
+  const Space space = space_of(P);
+  const Routing* R = space.routing;
+  const int slots = R->slots;
+  for (int i = threadIdx.x; i <= slots; i += kLayerThreads) {
+    experts[i < slots ? i : 0] = R->expert[i < slots ? i : 0];
+    first[i] = R->first[i];
   }
-  __syncthreads();
-  if (wave == 0) {
-    uint64_t word = (uint64_t(set.bits[2 * lane + 1]) << 32) | set.bits[2 * lane];
-    const int n = __popcll(word), upto = wave_scan_sum(n);
-    for (int i = upto - n; word; ++i, word &= word - 1) experts[i] = uint16_t(64 * lane + __builtin_ctzll(word));
-    if (lane == 63) total = upto;
-  }
+  for (int i = threadIdx.x; i < P.tokens * P.top_k; i += kLayerThreads) list[i] = R->rows[i];
+  for (int i = lane; i < P.tokens * 16; i += 64) sums[wave][i] = 0.f;
   __syncthreads();
   const int r = lane & 15, g = lane >> 4;
-  const int64_t c0 = 16 * int64_t(blockIdx.x);
+  const int tile = int(blockIdx.x) / splits, split = int(blockIdx.x) - tile * splits;
+  const int64_t c0 = 16 * int64_t(tile);
   const int cols = int(P.k - c0 < 16 ? P.k - c0 : 16);
-  const int64_t bytes = P.n * (I8 ? 1 : 2), part = part_of(P.n);
-  const int steps = int((bytes + 127) / 128), units = (steps + U - 1) / U;
-  const int64_t j = c0 + (r < cols ? r : cols - 1);
-  f32x4_t acc[MB];
-#pragma unroll
-  for (int m = 0; m < MB; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int all = __builtin_amdgcn_readfirstlane(total) * units;
-  for (int i = wave; i < all; i += kLayerWaves) {
-    const int slot = i / units, s0 = (i - slot * units) * U;
+  const int bytes = int(P.n) * (I8 ? 1 : 2), steps = (bytes + 127) / 128, units = (steps + U - 1) / U;
+  const int64_t part = part_of(P.n);
+  const char* const weights = static_cast<const char*>(P.w_out) + (c0 + (r < cols ? r : cols - 1)) * P.ld_out * (I8 ? 1 : 2);
+  const int64_t all = int64_t(slots) * units, runs = int64_t(splits) * W, run = int64_t(split) * W + wave;
+  const int from = int(all * run / runs), to = int(all * (run + 1) / runs);
+  int slot = from / units, unit = from - slot * units;
+  for (int i = from; i < to;) {
+    // one expert's units of this run, for sixteen of its rows at a time
     const int e = __builtin_amdgcn_readfirstlane(experts[slot]);
-    const char* wp = static_cast<const char*>(P.w_out) + (e * P.out_stride + j * P.ld_out) * (I8 ? 1 : 2);
-    const char* hp[MB];
-    bool has[MB];
+    const int lo = __builtin_amdgcn_readfirstlane(first[slot]), hi = __builtin_amdgcn_readfirstlane(first[slot + 1]);
+    const int n = units - unit < to - i ? units - unit : to - i;
+    const char* wp = weights + e * P.out_stride * (I8 ? 1 : 2);
+    f32x4_t scale = {1.f, 1.f, 1.f, 1.f};
+    if constexpr (I8) scale = four_scales(P.out_scale + e * P.k + c0, 4 * g, cols);
+    for (int r0 = lo; r0 < hi; r0 += 16) {
+      // rows past the last one read it again: their sums are not used
+      const bool has = r0 + r < hi;
+      const int row = list[has ? r0 + r : hi - 1], t = row >> 6;
+      const char* hp = reinterpret_cast<const char*>(space.h + (int64_t(t) * P.top_k + (row & 63)) * 2 * part);
+      f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+      for (int s0 = unit * U; s0 < (unit + n) * U; s0 += U) {
+        WeightStep<I8, MODE> w[U];
+        RowStep<I8, MODE> x[U][2][1];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const int t = 16 * m + r;
-      int pick = -1;
-      if (t < P.tokens)
-        for (int q = P.top_k - 1; q >= 0; --q)
-          if (ids[t * P.top_k + q] == e) pick = q;
-      has[m] = pick >= 0;
-      hp[m] = reinterpret_cast<const char*>(P.h + (int64_t(t) * P.top_k + (pick < 0 ? 0 : pick)) * 2 * part);
+        for (int u = 0; u < U; ++u) w[u].load(wp, (s0 + u) * 128, bytes, g);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            x[u][q][0].load(hp + q * part * 2, (s0 + u) * 128, bytes, g);
+        if ((s0 + U) * 128 > bytes) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            w[u].trim((s0 + u) * 128, bytes, g);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) x[u][q][0].trim((s0 + u) * 128, bytes, g);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) add_step<I8, MODE, 1>(w[u], x[u][q], acc);
+      }
+      // only the expert's own tokens: a weight that is not finite is nobody else's
+      if (has) {
+        f32x4_t* sum = reinterpret_cast<f32x4_t*>(&sums[wave][t * 16 + 4 * g]);
+        *sum += acc[0] * scale;
+      }
     }
-    WeightStep w[U];
-    RowStep<I8> x[U][2][MB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t at = int64_t(s0 + u) * 128;
-      w[u] = load_weight<I8, VEC>(wp, at, bytes, g);
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-          x[u][q][m] = load_row<I8, VEC>(hp[m] + q * part * 2, at, has[m] ? bytes : 0, g);
-    }
-    f32x4_t p[MB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) p[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) add_step<I8, MB>(w[u], x[u][q], p);
-    // only the expert's own tokens: a weight that is not finite is nobody else's
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float s = 1.f;
-      if constexpr (I8) s = P.out_scale[e * P.k + c0 + (4 * g + q < cols ? 4 * g + q : cols - 1)];
-#pragma unroll
-      for (int m = 0; m < MB; ++m) acc[m][q] = has[m] ? fmaf(s, p[m][q], acc[m][q]) : acc[m][q];
-    }
+    i += n;
+    unit = 0;
+    ++slot;
   }
-#pragma unroll
-  for (int m = 0; m < MB; ++m)
-    *reinterpret_cast<f32x4_t*>(sums + ((wave * MB + m) * 64 + lane) * 4) = acc[m];
   __syncthreads();
-  if (wave < MB) {
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  const int width = P.tokens * 16;
+  auto put = [&](int i, float v) {
+    if ((i & 15) < cols)
+      static_cast<uint16_t*>(P.y)[(i >> 4) * P.ldy + c0 + (i & 15)] = uint16_t(pack2_bf16(v, 0.f));
+  };
+  for (int i = threadIdx.x; i < width; i += kLayerThreads) {
+    float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kLayerWaves; ++w)
-      v += *reinterpret_cast<const f32x4_t*>(sums + ((w * MB + wave) * 64 + lane) * 4);
-    const int t = 16 * wave + r;
-    if (t < P.tokens) {
-      const float x[4] = {v[0], v[1], v[2], v[3]};
-      store4<uint16_t>(static_cast<uint16_t*>(P.y) + t * P.ldy + c0, 4 * g, cols, false, x);
-    }
+    for (int w = 0; w < W; ++w) v += sums[w][i];
+    if (splits == 1) put(i, v);
+    else __hip_atomic_store(&space.sums[(int64_t(tile) * splits + split) * width + i], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (splits == 1) return;
+  // The last of the blocks with these columns adds up their sums, in their order.
+  // The sums are written and read by atomics, which pass the XCDs' caches by, and
+  // are waited for before the block counts itself: so no fence is needed, which would write
+  // back and empty a whole L2 per block (588 us in place of FENCEUS).
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last_one = __hip_atomic_fetch_add(&space.arrived[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
+  __syncthreads();
+  if (!last_one) return;
+  for (int i = threadIdx.x; i < width; i += kLayerThreads) {
+    float v = 0.f;
+    for (int q = 0; q < splits; ++q)
+      v += __hip_atomic_load(&space.sums[(int64_t(tile) * splits + q) * width + i], __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+    put(i, v);
   }
 }
 
-template <bool I8, bool VEC>
+// Blocks that split the same columns: two per CU.
+int splits_of(int64_t k) {
+  const int64_t tiles = (k + 15) / 16, n = (2 * 256 + tiles - 1) / tiles;
+  return int(n < 1 ? 1 : n > 8 ? 8 : n);
+}
+
+template <bool I8, RowMode MODE>
 hipError_t launch_in(const LayerArgs& P, hipStream_t stream) {
   const int64_t picks = int64_t(P.tokens) * P.top_k, slots = picks < P.experts ? picks : P.experts;
-  const dim3 grid(static_cast<unsigned>(slots * ((P.n + 15) / 16))), block(kLayerThreads);
-  if (P.tokens <= 16) hipLaunchKernelGGL((layer_in_kernel<I8, VEC, 1>), grid, block, 0, stream, P);
-  else hipLaunchKernelGGL((layer_in_kernel<I8, VEC, 2>), grid, block, 0, stream, P);
+  const int64_t last = (P.n + 15) / 16;
+  // Waves: eight per tile, fewer where that still gives two rounds of all CUs' sixteen
+  const int64_t pieces = (P.k * (I8 ? 1 : 2) + 255) / 256;
+  int share = kLayerWaves;
+  while (share > 1 && (slots * last * (share / 2) >= 2 * 16 * 256 || share / 2 >= pieces)) share /= 2;
+  // tiles of a block: one round, and more where there are more than eight blocks per CU
+  const int64_t once = kLayerWaves / share;
+  int64_t rounds = slots * last / (once * 8 * 256);
+  rounds = rounds < 1 ? 1 : rounds > 8 ? 8 : rounds;
+  const int64_t tiles = rounds * once, groups = (last + tiles - 1) / tiles;
+  const dim3 grid(static_cast<unsigned>(slots * groups + 1)), block(kLayerThreads);
+  // two blocks of 16 rows where experts are likely to have more than 16
+  if (P.tokens > 16 && picks > 8 * int64_t(P.experts))
+    hipLaunchKernelGGL((layer_in_kernel<I8, MODE, 2>), grid, block, 0, stream, P, int(groups), int(tiles), share);
+  else
+    hipLaunchKernelGGL((layer_in_kernel<I8, MODE, 1>), grid, block, 0, stream, P, int(groups), int(tiles), share);
   return hipGetLastError();
 }
-template <bool I8, bool VEC>
+template <bool I8, RowMode MODE>
 hipError_t launch_out(const LayerArgs& P, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((P.k + 15) / 16)), block(kLayerThreads);
-  if (P.tokens <= 16) hipLaunchKernelGGL((layer_out_kernel<I8, VEC, 1>), grid, block, 0, stream, P);
-  else if (P.tokens <= 32) hipLaunchKernelGGL((layer_out_kernel<I8, VEC, 2>), grid, block, 0, stream, P);
-  else hipLaunchKernelGGL((layer_out_kernel<I8, VEC, 4>), grid, block, 0, stream, P);
+  const int splits = splits_of(P.k);
+  const dim3 grid(static_cast<unsigned>((P.k + 15) / 16 * splits)), block(kLayerThreads);
+  hipLaunchKernelGGL((layer_out_kernel<I8, MODE>), grid, block, 0, stream, P, splits);
   return hipGetLastError();
+}
+// `length`: of a weight row, in elements.
+template <bool I8>
+hipError_t launch_any(const LayerArgs& P, bool in, int64_t length, bool vec, hipStream_t stream) {
+  if (length * (I8 ? 1 : 2) < 16) return in ? launch_in<I8, kSingle>(P, stream) : launch_out<I8, kSingle>(P, stream);
+  if (!vec) return in ? launch_in<I8, kMoved>(P, stream) : launch_out<I8, kMoved>(P, stream);
+  return in ? launch_in<I8, kWhole>(P, stream) : launch_out<I8, kWhole>(P, stream);
 }
 
 }  // namespace
 
+int64_t layer_workspace(const LayerArgs& P) {
+  const Space s = space_of(P);
+  const int splits = splits_of(P.k);
+  const int64_t sums = splits > 1 ? 4 * (P.k + 15) / 16 * 16 * P.tokens * splits : 0;
+  return reinterpret_cast<char*>(s.sums) - static_cast<char*>(P.workspace) + whole(sums);
+}
+
 hipError_t launch_layer_in(const LayerArgs& P, bool vec, hipStream_t stream) {
-  if (P.in_scale) return vec ? launch_in<true, true>(P, stream) : launch_in<true, false>(P, stream);
-  return vec ? launch_in<false, true>(P, stream) : launch_in<false, false>(P, stream);
+  return P.in_scale ? launch_any<true>(P, true, P.k, vec, stream) : launch_any<false>(P, true, P.k, vec, stream);
 }
 hipError_t launch_layer_out(const LayerArgs& P, bool vec, hipStream_t stream) {
-  if (P.in_scale) return vec ? launch_out<true, true>(P, stream) : launch_out<true, false>(P, stream);
-  return vec ? launch_out<false, true>(P, stream) : launch_out<false, false>(P, stream);
+  return P.in_scale ? launch_any<true>(P, false, P.n, vec, stream) : launch_any<false>(P, false, P.n, vec, stream);
 }
 
 }  // namespace dmuon

@@ -270,9 +270,14 @@ int dmuon_row_matmul(const dmuon_row_product_t* d, const void* a, const float* a
 
 size_t dmuon_expert_layer_workspace_size(const dmuon_expert_layer_t* d) {
   if (!d || d->tokens < 1 || d->tokens > kLayerTokens || d->top_k < 1 || d->top_k > kLayerPicks || d->n < 1 ||
-      d->n > kMaxDim)
+      d->n > kMaxDim || d->k < 1 || d->k > kMaxDim)
     return 0;
-  return static_cast<size_t>(d->tokens * d->top_k * up(d->n, 8) * 32);
+  LayerArgs P = {};
+  P.tokens = static_cast<int32_t>(d->tokens);
+  P.top_k = d->top_k;
+  P.n = d->n;
+  P.k = d->k;
+  return static_cast<size_t>(layer_workspace(P));
 }
 
 int dmuon_expert_layer(const dmuon_expert_layer_t* d, const void* x, const int32_t* ids, const float* gates,
@@ -311,28 +316,28 @@ int dmuon_expert_layer(const dmuon_expert_layer_t* d, const void* x, const int32
                       {out_scale, 4 * d->experts * d->k, "out_scale"}}, 2);
     if (st) return st;
     const int64_t slots = picks < d->experts ? picks : d->experts;
-    if (slots * up(d->n, 16) > (int64_t(1) << 22))
+    if (slots * up(d->n, 16) >= (int64_t(1) << 22))
       return set_last_error(DMUON_ERR_UNSUPPORTED, "more than 2^22 pieces of 16 columns");
     st = check_current_device();
     if (st) return st;
     LayerArgs P = {};
     P.x = x; P.ids = ids; P.gates = gates; P.w_in = w_in; P.in_scale = in_scale; P.w_out = w_out; P.out_scale = out_scale;
-    P.y = y; P.h = static_cast<uint16_t*>(workspace);
+    P.y = y; P.workspace = workspace;
     P.n = d->n; P.k = d->k; P.ldx = d->ldx; P.ldy = d->ldy; P.ld_in = d->ld_in; P.ld_out = d->ld_out;
     P.in_stride = in_stride; P.out_stride = out_stride;
     P.tokens = static_cast<int32_t>(d->tokens); P.experts = d->experts; P.top_k = d->top_k;
-    // whole 16-byte chunks along every row
-    const bool vec = aligned(x, 16) && aligned(w_in, 16) && aligned(w_out, 16) && d->ldx % 8 == 0 &&
-                     d->k * ws % 16 == 0 && d->n * ws % 16 == 0 && d->ld_in * ws % 16 == 0 && d->ld_out * ws % 16 == 0 &&
-                     in_stride * ws % 16 == 0 && out_stride * ws % 16 == 0;
+    // whole 16-byte chunks along every row of a product's operands
+    const bool vec_in = aligned(x, 16) && aligned(w_in, 16) && d->ldx % 8 == 0 && d->k * ws % 16 == 0 &&
+                        d->ld_in * ws % 16 == 0 && in_stride * ws % 16 == 0;
+    const bool vec_out = aligned(w_out, 16) && d->n * ws % 16 == 0 && d->ld_out * ws % 16 == 0 && out_stride * ws % 16 == 0;
     const hipStream_t stream = static_cast<hipStream_t>(stream_);
     const int64_t weights = slots * d->n * d->k * ws;
     st = hip_status(profiled_launch(PK_LAYER_IN, product_flops(picks, 2 * d->n, d->k), 2 * weights, stream,
-                                    [&] { return launch_layer_in(P, vec, stream); }),
+                                    [&] { return launch_layer_in(P, vec_in, stream); }),
                     "expert_layer");
     if (st) return st;
     return hip_status(profiled_launch(PK_LAYER_OUT, product_flops(picks, d->n, d->k), weights, stream,
-                                      [&] { return launch_layer_out(P, vec, stream); }),
+                                      [&] { return launch_layer_out(P, vec_out, stream); }),
                       "expert_layer");
   });
 }
