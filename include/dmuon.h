@@ -552,7 +552,7 @@ int dmuon_block_matmul(const dmuon_block_product_t* d, const void* a, const floa
  * parameters of its neighbours follow from the next step on.
  * Tensors without a gradient (NULL) or elements are left as they are.  Any
  * numel 0..2^42, buffers aligned to their elements.  No workspace: the tables
- * travel as kernel arguments (40 tensors and 16 groups per launch).  A captured
+ * travel as kernel arguments (48 tensors and 16 groups per launch).  A captured
  * call repeats its step number on replay.
  * Errors as for dmuon_adamw_step; no two buffers may overlap.
  */

@@ -10,7 +10,9 @@ raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import json
+import operator
 import os
 import struct
 from typing import List, Optional, Sequence, Tuple
@@ -560,6 +562,30 @@ _STATE_BLOCK = 128
 _ADAMW8_TENSOR = struct.Struct("<7q4i")      # dmuon_adamw_quantized_t
 
 
+_dtype_of = operator.attrgetter("dtype")
+_STATE, _SCALE = {torch.float8_e4m3fn}, {torch.float32}
+
+
+def _refuse_states(params, grads, exp_avgs, roots, exp_avg_scales, root_scales, device) -> None:
+    """Says which tensors of dmuon_adamw_step_quantized do not fit, and why (the
+    checks there take all of them at once: a call's host time is theirs)."""
+    for i, (p, g, m, r, ms, rs) in enumerate(zip(params, grads, exp_avgs, roots, exp_avg_scales, root_scales)):
+        every, numel = (p, g, m, r, ms, rs), p.numel()
+        blocks = (numel + _STATE_BLOCK - 1) // _STATE_BLOCK
+        if {m.dtype, r.dtype} != _STATE or {ms.dtype, rs.dtype} != _SCALE:
+            raise TypeError(f"tensors[{i}]: states must be float8_e4m3fn, their scales float32")
+        if p.dtype not in _DTYPES or g.dtype not in _DTYPES:
+            raise TypeError(f"tensors[{i}]: unsupported dtype")
+        if {m.numel(), r.numel(), g.numel()} != {numel} or {ms.numel(), rs.numel()} != {blocks}:
+            raise ValueError(f"tensors[{i}]: gradient and states must have the parameter's size, scales one value per "
+                             "128 elements")
+        if not all(t.is_contiguous() for t in every):
+            raise ValueError(f"tensors[{i}] must be contiguous")
+        if any(t.device != device for t in every):
+            raise ValueError(f"tensors[{i}] must be on {device}")
+    raise ValueError("tensors do not fit together")
+
+
 def dmuon_adamw_quantized_state(param: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """(exp_avg, exp_avg_scale, root, root_scale) of a parameter before its first
     dmuon_adamw_step_quantized: zeros."""
@@ -600,32 +626,29 @@ def dmuon_adamw_step_quantized(params: Sequence[torch.Tensor], grads: Sequence[O
         ga[k] = dmuon_adamw_group_t(float(h.get("lr", 1e-3)), float(b1), float(b2), float(h.get("eps", 1e-8)),
                                     float(h.get("weight_decay", 0.01)), int(h["step"]))
     device = _gpu(params[0])
-    f8, f32, table, pack = torch.float8_e4m3fn, torch.float32, [], _ADAMW8_TENSOR.pack
-    for i, (p, g, m, ms, r, rs) in enumerate(zip(params, grads, exp_avgs, exp_avg_scales, roots, root_scales)):
-        numel = p.numel()
-        if m.dtype != f8 or r.dtype != f8 or ms.dtype != f32 or rs.dtype != f32:
-            raise TypeError(f"tensors[{i}]: states must be float8_e4m3fn, their scales float32")
-        blocks = (numel + _STATE_BLOCK - 1) // _STATE_BLOCK
-        if m.numel() != numel or r.numel() != numel or ms.numel() != blocks or rs.numel() != blocks:
-            raise ValueError(f"tensors[{i}]: states must have the parameter's size, scales one value per 128 elements")
-        if not (p.is_contiguous() and m.is_contiguous() and ms.is_contiguous() and r.is_contiguous()
-                and rs.is_contiguous()):
-            raise ValueError(f"tensors[{i}] must be contiguous")
-        dt = _DTYPES.get(p.dtype)
-        gdt, gp = dt, 0
-        if g is not None:
-            if g.numel() != numel or not g.is_contiguous():
-                raise ValueError(f"grads[{i}] must be contiguous and of the parameter's size")
-            gdt, gp = _DTYPES.get(g.dtype), g.data_ptr()
-            if g.device != device:
-                raise ValueError(f"a tensor is on {g.device}, not {device}")
-        if dt is None or gdt is None:
-            raise TypeError(f"tensors[{i}]: unsupported dtype")
-        if p.device != device or m.device != device or ms.device != device or r.device != device or rs.device != device:
-            raise ValueError(f"tensors[{i}] must be on {device}")
-        table.append(pack(numel, p.data_ptr(), gp, m.data_ptr(), ms.data_ptr(), r.data_ptr(), rs.data_ptr(), dt, gdt,
-                          int(group_index[i]), 0))
-    _launch(_lib.dmuon_adamw_step_quantized, "dmuon_adamw_step_quantized", device, stream, b"".join(table), n, ga,
+    states = (exp_avgs, roots, exp_avg_scales, root_scales)
+    skipped = [g is None for g in grads]
+    given = [p if g is None else g for p, g in zip(params, grads)] if True in skipped else grads
+    size, kind = torch.Tensor.numel, _dtype_of
+    numels = list(map(size, params))
+    blocks = [(v + _STATE_BLOCK - 1) // _STATE_BLOCK for v in numels]
+    pdt, gdt = ([_DTYPES.get(t) for t in map(kind, ts)] for ts in (params, given))
+    every = list(itertools.chain(params, given, *states))
+    if not (list(map(size, given)) == numels and list(map(size, exp_avgs)) == numels
+            and list(map(size, roots)) == numels and list(map(size, exp_avg_scales)) == blocks
+            and list(map(size, root_scales)) == blocks and set(map(kind, exp_avgs)) == set(map(kind, roots)) == _STATE
+            and set(map(kind, exp_avg_scales)) == set(map(kind, root_scales)) == _SCALE
+            and None not in pdt and None not in gdt and all(map(torch.Tensor.is_contiguous, every))
+            and set(map(torch.Tensor.get_device, every)) == {device.index}):
+        _refuse_states(params, given, *states, device)
+    ptr = torch.Tensor.data_ptr
+    grad_ptrs = map(ptr, given)
+    if given is not grads:
+        grad_ptrs = [0 if skip else q for skip, q in zip(skipped, grad_ptrs)]
+    table = b"".join(map(_ADAMW8_TENSOR.pack, numels, map(ptr, params), grad_ptrs, map(ptr, exp_avgs),
+                         map(ptr, exp_avg_scales), map(ptr, roots), map(ptr, root_scales), pdt, gdt,
+                         map(int, group_index), itertools.repeat(0)))
+    _launch(_lib.dmuon_adamw_step_quantized, "dmuon_adamw_step_quantized", device, stream, table, n, ga,
             len(groups), int(seed))
 
 

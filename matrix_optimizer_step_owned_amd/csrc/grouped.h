@@ -218,6 +218,33 @@ __device__ __forceinline__ u32x4_t moved_down(const u32x4_t& w, int gone) {
   return u32x4_t{uint32_t(l), uint32_t(l >> 32), uint32_t(h), uint32_t(h >> 32)};
 }
 
+// Rows of any alignment and length are read in one of three ways.  kWhole: aligned,
+// a multiple of 16 bytes.  kMoved: at least 16 bytes long.  Both read a chunk that
+// ends past the row from further down, where the row ends, and put it right before it is
+// used (trim).  kSingle: shorter, element by element.
+enum RowMode { kWhole, kMoved, kSingle };
+
+template <int EB, RowMode MODE>
+__device__ __forceinline__ u32x4_t row_chunk(const char* row, int at, int bytes) {
+  if constexpr (MODE == kSingle) {
+    const int left = (bytes - at) / EB;
+    return load_chunk<EB, false>(row + at, left < 0 ? 0 : left > 16 / EB ? 16 / EB : left);
+  } else {
+    struct __attribute__((packed, aligned(MODE == kWhole ? 16 : EB))) Any { u32x4_t v; };
+    return reinterpret_cast<const Any*>(row + (at < bytes - 16 ? at : bytes - 16))->v;
+  }
+}
+template <RowMode MODE>
+__device__ __forceinline__ void trim_chunk(u32x4_t& v, int at, int bytes) {
+  const int gone = at - (bytes - 16);
+  if constexpr (MODE == kWhole) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = gone > 0 ? 0u : v[i];
+  } else if constexpr (MODE == kMoved) {
+    if (gone > 0) v = moved_down(v, gone);
+  }
+}
+
 // Buffer descriptor of `bytes` bytes at `base` (raw buffer, no stride), in
 // scalar registers; a lane whose offset is outside reads zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t slab_rsrc(const void* base, uint32_t bytes) {

@@ -239,9 +239,30 @@ __device__ __forceinline__ f32x4_t scaled(const i32x4_t& sum, float sa, const f3
                  float(sum[3]) * sa * sb[3]};
 }
 
+// One thread's share of an operand's stage of 128 k, TILE / 32 chunks; rows past the
+// last one read it again: their results are not stored.
+template <int TILE, RowMode MODE>
+struct Int8Stage {
+  u32x4_t v[TILE / 32];
+  __device__ __forceinline__ void load(const char* base, int64_t ld, int rows, int at, int k) {
+#pragma unroll
+    for (int q = 0; q < TILE / 32; ++q) {
+      const int r = (int(threadIdx.x) >> 3) + 32 * q;
+      v[q] = row_chunk<1, MODE>(base + (r < rows ? r : rows - 1) * ld, at + (threadIdx.x & 7) * 16, k);
+    }
+  }
+  __device__ __forceinline__ void write(char* lds, int at, int k) {
+    if (at + 128 > k) {
+#pragma unroll
+      for (int q = 0; q < TILE / 32; ++q) trim_chunk<MODE>(v[q], at + (threadIdx.x & 7) * 16, k);
+    }
+    write_stage<TILE>(lds, v);
+  }
+};
+
 // Tiles of 128 or 64, four waves in 2 x 2, operands staged through registers
 // and a two-slot LDS ring; any alignment.  Stages in flight as in block_matmul_kernel.
-template <bool VEC, int TILE, typename OutT>
+template <RowMode MODE, int TILE, typename OutT>
 __global__ void __launch_bounds__(kStageThreads, 2)
 int8_matmul_kernel(Int8Args P) {
   constexpr int kStep = 128;       // k per stage
@@ -276,17 +297,18 @@ int8_matmul_kernel(Int8Args P) {
   for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < F; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
-  u32x4_t va[D][TILE / 32], vb[D][TILE / 32];
+  const int k = int(P.k);
+  Int8Stage<TILE, MODE> va[D], vb[D];
   auto load = [&](int st, int d) {
     if (st < stages) {
-      load_stage<TILE, VEC>(a, P.lda, rows, int64_t(st) * kStep, P.k, va[d]);
-      load_stage<TILE, VEC>(b, P.ldb, cols, int64_t(st) * kStep, P.k, vb[d]);
+      va[d].load(a, P.lda, rows, st * kStep, k);
+      vb[d].load(b, P.ldb, cols, st * kStep, k);
     }
   };
   auto write = [&](int st, int d) {
     if (st < stages) {
-      write_stage<TILE>(smem + (st & 1) * 2 * OPB, va[d]);
-      write_stage<TILE>(smem + (st & 1) * 2 * OPB + OPB, vb[d]);
+      va[d].write(smem + (st & 1) * 2 * OPB, st * kStep, k);
+      vb[d].write(smem + (st & 1) * 2 * OPB + OPB, st * kStep, k);
     }
   };
 #pragma unroll
@@ -505,6 +527,14 @@ hipError_t launch_skinny(const Int8Args& P, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int TILE, typename OutT>
+void launch_tiles(const Int8Args& P, bool vec, dim3 grid, hipStream_t stream) {
+  const dim3 block(kStageThreads);
+  if (vec) hipLaunchKernelGGL((int8_matmul_kernel<kWhole, TILE, OutT>), grid, block, 0, stream, P);
+  else if (P.k >= 16) hipLaunchKernelGGL((int8_matmul_kernel<kMoved, TILE, OutT>), grid, block, 0, stream, P);
+  else hipLaunchKernelGGL((int8_matmul_kernel<kSingle, TILE, OutT>), grid, block, 0, stream, P);
+}
+
 template <typename OutT>
 hipError_t launch_matmul(const Int8Args& P, bool vec, hipStream_t stream) {
   const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
@@ -528,14 +558,9 @@ hipError_t launch_matmul(const Int8Args& P, bool vec, hipStream_t stream) {
   // 64-tiles where 128-tiles would give fewer than one per CU
   auto tiles = [&](int64_t t) { return (P.m / t + used) * ((P.n + t - 1) / t); };
   const bool small = tiles(128) < 256 && tiles(64) <= kMaxSkinnyBlocks;
-  const dim3 grid(static_cast<unsigned>(grouped_grid(tiles(small ? 64 : 128)))), block(kStageThreads);
-  if (small) {
-    if (vec) hipLaunchKernelGGL((int8_matmul_kernel<true, 64, OutT>), grid, block, 0, stream, P);
-    else hipLaunchKernelGGL((int8_matmul_kernel<false, 64, OutT>), grid, block, 0, stream, P);
-  } else {
-    if (vec) hipLaunchKernelGGL((int8_matmul_kernel<true, 128, OutT>), grid, block, 0, stream, P);
-    else hipLaunchKernelGGL((int8_matmul_kernel<false, 128, OutT>), grid, block, 0, stream, P);
-  }
+  const dim3 grid(static_cast<unsigned>(grouped_grid(tiles(small ? 64 : 128))));
+  if (small) launch_tiles<64, OutT>(P, vec, grid, stream);
+  else launch_tiles<128, OutT>(P, vec, grid, stream);
   return hipGetLastError();
 }
 

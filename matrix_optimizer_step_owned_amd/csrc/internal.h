@@ -179,7 +179,7 @@ struct Adam8Group {      // as AdamItem has them
 constexpr int kAdam8Threads = 256;
 constexpr int kAdam8Chunk = 8192;      // elements of one tensor per block
 constexpr int kAdam8Block = 128;       // elements per scale
-constexpr int kAdam8Tensors = 40;      // of one launch: a table of 3.4 KB
+constexpr int kAdam8Tensors = 48;      // of one launch: a table of 3976 bytes
 constexpr int kAdam8Groups = 16;
 constexpr int64_t kMaxAdam8Blocks = int64_t(1) << 23;   // of one launch: fewer than 2^32 threads
 struct Adam8Table {
@@ -187,6 +187,7 @@ struct Adam8Table {
   Adam8Group groups[kAdam8Groups];
   int32_t n;
 };
+static_assert(sizeof(Adam8Table) <= 4096, "a kernel's arguments");
 // Key of a tensor's random numbers.
 uint32_t adamw8_key(uint32_t seed, int64_t step, uint32_t tensor);
 hipError_t launch_adamw8(const Adam8Table& table, int64_t nblocks, hipStream_t stream);

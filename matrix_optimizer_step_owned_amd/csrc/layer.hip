@@ -48,33 +48,6 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// Rows of any alignment and length are read in one of three ways.  kWhole: aligned,
-// a multiple of 16 bytes.  kMoved: at least 16 bytes long.  Both read a chunk that
-// ends past the row from further down, where the row ends, and put it right before it is
-// used (trim).  kSingle: shorter, element by element.
-enum RowMode { kWhole, kMoved, kSingle };
-
-template <int EB, RowMode MODE>
-__device__ __forceinline__ u32x4_t row_chunk(const char* row, int at, int bytes) {
-  if constexpr (MODE == kSingle) {
-    const int left = (bytes - at) / EB;
-    return load_chunk<EB, false>(row + at, left < 0 ? 0 : left > 16 / EB ? 16 / EB : left);
-  } else {
-    struct __attribute__((packed, aligned(MODE == kWhole ? 16 : EB))) Any { u32x4_t v; };
-    return reinterpret_cast<const Any*>(row + (at < bytes - 16 ? at : bytes - 16))->v;
-  }
-}
-template <RowMode MODE>
-__device__ __forceinline__ void trim_chunk(u32x4_t& v, int at, int bytes) {
-  const int gone = at - (bytes - 16);
-  if constexpr (MODE == kWhole) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = gone > 0 ? 0u : v[i];
-  } else if constexpr (MODE == kMoved) {
-    if (gone > 0) v = moved_down(v, gone);
-  }
-}
-
 // One step (128 bytes of a weight row) of the weights and of the rows that they
 // multiply: a bf16 row has 128 bytes of it, or 256 with 8-bit weights.  `at`,
 // `bytes`: of the weight row.

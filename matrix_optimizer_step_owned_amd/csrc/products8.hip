@@ -60,9 +60,9 @@ int adamw8_step(const dmuon_adamw_quantized_t* tensors, int32_t n, const dmuon_a
     f.one_minus_beta2 = static_cast<float>(1.0 - G.beta2);
   }
   std::vector<int> active;
-  std::vector<Written> spans;
+  std::vector<Written> spans[6], both;
   active.reserve(n);
-  spans.reserve(6 * size_t(n));
+  for (auto& s : spans) s.reserve(n);
   for (int i = 0; i < n; ++i) {
     const dmuon_adamw_quantized_t& T = tensors[i];
     if (T.numel < 0 || T.numel > kMaxNumel) return bad(state_name(i) + ".numel must be in 0..2^42");
@@ -82,15 +82,24 @@ int adamw8_step(const dmuon_adamw_quantized_t* tensors, int32_t n, const dmuon_a
                               T.numel, scales};
     for (int w = 0; w < 6; ++w) {
       const uintptr_t lo = reinterpret_cast<uintptr_t>(p[w]);
-      spans.push_back({lo, lo + uintptr_t(bytes[w]), i, w});
+      spans[w].push_back({lo, lo + uintptr_t(bytes[w]), i, w});
     }
   }
   if (active.empty()) return DMUON_OK;
-  std::sort(spans.begin(), spans.end(), [](const Written& a, const Written& b) { return a.lo < b.lo; });
-  for (size_t i = 1; i < spans.size(); ++i)
-    if (spans[i].lo < spans[i - 1].hi)
-      return set_last_error(DMUON_ERR_ALIASING, state_name(spans[i - 1].tensor, spans[i - 1].what) + " overlaps " +
-                                                    state_name(spans[i].tensor, spans[i].what));
+  // in order of their addresses; pieces of flat buffers come in order already
+  auto before = [](const Written& a, const Written& b) { return a.lo < b.lo; };
+  for (int w = 0; w < 6; ++w) {
+    if (!std::is_sorted(spans[w].begin(), spans[w].end(), before)) std::sort(spans[w].begin(), spans[w].end(), before);
+    if (w == 0) continue;
+    both.resize(spans[0].size() + spans[w].size());
+    std::merge(spans[0].begin(), spans[0].end(), spans[w].begin(), spans[w].end(), both.begin(), before);
+    spans[0].swap(both);
+  }
+  const std::vector<Written>& all = spans[0];
+  for (size_t i = 1; i < all.size(); ++i)
+    if (all[i].lo < all[i - 1].hi)
+      return set_last_error(DMUON_ERR_ALIASING, state_name(all[i - 1].tensor, all[i - 1].what) + " overlaps " +
+                                                    state_name(all[i].tensor, all[i].what));
   int st = check_current_device();
   if (st) return st;
   const hipStream_t stream = static_cast<hipStream_t>(stream_);
