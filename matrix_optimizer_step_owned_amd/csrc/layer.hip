@@ -258,7 +258,7 @@ __device__ __forceinline__ void list_rows(const LayerArgs& P, const Ids& ids, Ro
 // Tiles of sixteen columns of h (16 rows of G and of U) of one expert, `tiles` of them per
 // block.  `share` waves split the sum of a tile: one where there are tiles for all
 // waves, which then neither wait nor add up (32 tokens, 8 of 128 experts of 1024 x
-// 2048 in 8 bits: 137 us with eight, SHAREUS with one); otherwise they add up in LDS in
+// 2048 in 8 bits: 137 us with eight, 87 with one); otherwise they add up in LDS in
 // wave order, one wave for all, another for each round, while the others go on.
 template <bool I8, RowMode MODE, int MB>
 __global__ void __launch_bounds__(kLayerThreads, MB == 1 ? 4 : 2)
@@ -425,35 +425,49 @@ layer_in_kernel(LayerArgs P, int groups, int tiles, int share) {
   }
 }
 
-// Sixteen columns of y for all tokens, or one of `splits` parts of their sums.  The
+// kOutCols columns of y for all tokens, or one of `splits` parts of their sums.  The
 // sums run over units: U steps of an expert's rows.  Every wave has a run of
-// them and keeps 16 rows' sums in registers while the expert stays the same.
+// them and keeps 16 rows' sums in registers while the expert stays the same.  A
+// load of h, with its two parts and rows that 16 lanes share, takes the load path as long as one of
+// weights, so each serves two blocks of 16 columns (one token, two experts of
+// 14336 x 4096: 54.7 us with one block, 47.0 with two, 46.5 with four; the 32 tokens in 8 bits
+// 62.5, 48.4, 57.4).
+constexpr int kOutBlocks = 2, kOutCols = 16 * kOutBlocks;
+constexpr int kMaxSplits = 16;
 template <bool I8, RowMode MODE>
 __global__ void __launch_bounds__(kLayerThreads, 4)
 layer_out_kernel(LayerArgs P, int splits) {
-  constexpr int U = (I8 ? 2 : 4) / (MODE == kWhole ? 1 : 2), W = kLayerWaves;
+  constexpr int U = I8 ? 1 : 2, W = kLayerWaves, NB = kOutBlocks;
   __shared__ uint16_t experts[kLayerExperts], first[kLayerExperts + 1];
   __shared__ uint16_t list[kLayerTokens * kLayerPicks];
-  __shared__ __attribute__((aligned(16))) float sums[W][kLayerTokens * 16];
+  extern __shared__ __attribute__((aligned(16))) float sums[];      // W x tokens x kOutCols
   __shared__ int last_one;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Space space = space_of(P);
   const Routing* R = space.routing;
-  const int slots = R->slots;
-  for (int i = threadIdx.x; i <= slots; i += kLayerThreads) {
-    experts[i < slots ? i : 0] = R->expert[i < slots ? i : 0];
+  // as many entries as there can be, without waiting for how many there are
+  const int picks = P.tokens * P.top_k, most = picks < P.experts ? picks : P.experts, slots = R->slots;
+  for (int i = threadIdx.x; i <= most; i += kLayerThreads) {
+    if (i < most) experts[i] = R->expert[i];
     first[i] = R->first[i];
   }
-  for (int i = threadIdx.x; i < P.tokens * P.top_k; i += kLayerThreads) list[i] = R->rows[i];
-  for (int i = lane; i < P.tokens * 16; i += 64) sums[wave][i] = 0.f;
+  for (int i = threadIdx.x; i < picks; i += kLayerThreads) list[i] = R->rows[i];
+  const int width = P.tokens * kOutCols;
+  for (int i = threadIdx.x; i < W * width; i += kLayerThreads) sums[i] = 0.f;
   __syncthreads();
   const int r = lane & 15, g = lane >> 4;
   const int tile = int(blockIdx.x) / splits, split = int(blockIdx.x) - tile * splits;
-  const int64_t c0 = 16 * int64_t(tile);
-  const int cols = int(P.k - c0 < 16 ? P.k - c0 : 16);
+  const int64_t c0 = kOutCols * int64_t(tile);
+  const int cols = int(P.k - c0 < kOutCols ? P.k - c0 : kOutCols);
   const int bytes = int(P.n) * (I8 ? 1 : 2), steps = (bytes + 127) / 128, units = (steps + U - 1) / U;
   const int64_t part = part_of(P.n);
-  const char* const weights = static_cast<const char*>(P.w_out) + (c0 + (r < cols ? r : cols - 1)) * P.ld_out * (I8 ? 1 : 2);
+  // columns past the end read the last one: their sums are not used
+  const char* weights[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int c = 16 * b + r;
+    weights[b] = static_cast<const char*>(P.w_out) + (c0 + (c < cols ? c : cols - 1)) * P.ld_out * (I8 ? 1 : 2);
+  }
   const int64_t all = int64_t(slots) * units, runs = int64_t(splits) * W, run = int64_t(split) * W + wave;
   const int from = int(all * run / runs), to = int(all * (run + 1) / runs);
   int slot = from / units, unit = from - slot * units;
@@ -462,20 +476,28 @@ layer_out_kernel(LayerArgs P, int splits) {
     const int e = __builtin_amdgcn_readfirstlane(experts[slot]);
     const int lo = __builtin_amdgcn_readfirstlane(first[slot]), hi = __builtin_amdgcn_readfirstlane(first[slot + 1]);
     const int n = units - unit < to - i ? units - unit : to - i;
-    const char* wp = weights + e * P.out_stride * (I8 ? 1 : 2);
-    f32x4_t scale = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (I8) scale = four_scales(P.out_scale + e * P.k + c0, 4 * g, cols);
+    const int64_t expert = e * P.out_stride * (I8 ? 1 : 2);
+    f32x4_t scale[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      scale[b] = f32x4_t{1.f, 1.f, 1.f, 1.f};
+      if constexpr (I8) scale[b] = four_scales(P.out_scale + e * P.k + c0, 16 * b + 4 * g, cols);
+    }
     for (int r0 = lo; r0 < hi; r0 += 16) {
       // rows past the last one read it again: their sums are not used
       const bool has = r0 + r < hi;
       const int row = list[has ? r0 + r : hi - 1], t = row >> 6;
       const char* hp = reinterpret_cast<const char*>(space.h + (int64_t(t) * P.top_k + (row & 63)) * 2 * part);
-      f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+      f32x4_t acc[NB][1];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[b][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       for (int s0 = unit * U; s0 < (unit + n) * U; s0 += U) {
-        WeightStep<I8, MODE> w[U];
+        WeightStep<I8, MODE> w[U][NB];
         RowStep<I8, MODE> x[U][2][1];
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u].load(wp, (s0 + u) * 128, bytes, g);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) w[u][b].load(weights[b] + expert, (s0 + u) * 128, bytes, g);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -484,7 +506,8 @@ layer_out_kernel(LayerArgs P, int splits) {
         if ((s0 + U) * 128 > bytes) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            w[u].trim((s0 + u) * 128, bytes, g);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) w[u][b].trim((s0 + u) * 128, bytes, g);
 #pragma unroll
             for (int q = 0; q < 2; ++q) x[u][q][0].trim((s0 + u) * 128, bytes, g);
           }
@@ -492,12 +515,19 @@ layer_out_kernel(LayerArgs P, int splits) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) add_step<I8, MODE, 1>(w[u], x[u][q], acc);
+          for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) add_step<I8, MODE, 1>(w[u][b], x[u][q], acc[b]);
+            if constexpr (I8) __builtin_amdgcn_sched_barrier(0);    // one widened step at a time
+          }
       }
       // only the expert's own tokens: a weight that is not finite is nobody else's
       if (has) {
-        f32x4_t* sum = reinterpret_cast<f32x4_t*>(&sums[wave][t * 16 + 4 * g]);
-        *sum += acc[0] * scale;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          f32x4_t* sum = reinterpret_cast<f32x4_t*>(&sums[wave * width + t * kOutCols + 16 * b + 4 * g]);
+          *sum += acc[b][0] * scale[b];
+        }
       }
     }
     i += n;
@@ -505,15 +535,14 @@ layer_out_kernel(LayerArgs P, int splits) {
     ++slot;
   }
   __syncthreads();
-  const int width = P.tokens * 16;
   auto put = [&](int i, float v) {
-    if ((i & 15) < cols)
-      static_cast<uint16_t*>(P.y)[(i >> 4) * P.ldy + c0 + (i & 15)] = uint16_t(pack2_bf16(v, 0.f));
+    const int t = i / kOutCols, c = i % kOutCols;
+    if (c < cols) static_cast<uint16_t*>(P.y)[t * P.ldy + c0 + c] = uint16_t(pack2_bf16(v, 0.f));
   };
   for (int i = threadIdx.x; i < width; i += kLayerThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += sums[w][i];
+    for (int w = 0; w < W; ++w) v += sums[w * width + i];
     if (splits == 1) put(i, v);
     else __hip_atomic_store(&space.sums[(int64_t(tile) * splits + split) * width + i], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
@@ -521,7 +550,7 @@ layer_out_kernel(LayerArgs P, int splits) {
   // The last of the blocks with these columns adds up their sums, in their order.
   // The sums are written and read by atomics, which pass the XCDs' caches by, and
   // are waited for before the block counts itself: so no fence is needed, which would write
-  // back and empty a whole L2 per block (588 us in place of FENCEUS).
+  // back and empty a whole L2 per block (588 us in place of 54).
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0)
@@ -529,24 +558,37 @@ layer_out_kernel(LayerArgs P, int splits) {
   __syncthreads();
   if (!last_one) return;
   for (int i = threadIdx.x; i < width; i += kLayerThreads) {
-    float v = 0.f;
-    for (int q = 0; q < splits; ++q)
-      v += __hip_atomic_load(&space.sums[(int64_t(tile) * splits + q) * width + i], __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
+    float part[kMaxSplits], v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kMaxSplits; ++q)
+      if (q < splits)
+        part[q] = __hip_atomic_load(&space.sums[(int64_t(tile) * splits + q) * width + i], __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int q = 0; q < kMaxSplits; ++q)
+      if (q < splits) v += part[q];
     put(i, v);
   }
 }
 
-// Blocks that split the same columns: two per CU.
-int splits_of(int64_t k) {
-  const int64_t tiles = (k + 15) / 16, n = (2 * 256 + tiles - 1) / tiles;
-  return int(n < 1 ? 1 : n > 8 ? 8 : n);
+int64_t out_tiles(int64_t k) { return (k + kOutCols - 1) / kOutCols; }
+int64_t slots_of(const LayerArgs& P) {
+  const int64_t picks = int64_t(P.tokens) * P.top_k;
+  return picks < P.experts ? picks : P.experts;
+}
+// Blocks that split the same columns: two per CU, or one with 8-bit weights (both
+// kinds with one and two: the 32 tokens 48.4 and 53.2 us, one token in bf16 48.5 and 47.0),
+// as long as every wave has two units (of 128 elements) where all experts are touched.
+int splits_of(const LayerArgs& P, bool i8) {
+  const int64_t tiles = out_tiles(P.k), units = slots_of(P) * ((P.n + 127) / 128);
+  int64_t n = ((i8 ? 256 : 512) + tiles - 1) / tiles;
+  if (n > units / (2 * kLayerWaves)) n = units / (2 * kLayerWaves);
+  return int(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
 
 template <bool I8, RowMode MODE>
 hipError_t launch_in(const LayerArgs& P, hipStream_t stream) {
-  const int64_t picks = int64_t(P.tokens) * P.top_k, slots = picks < P.experts ? picks : P.experts;
-  const int64_t last = (P.n + 15) / 16;
+  const int64_t picks = int64_t(P.tokens) * P.top_k, slots = slots_of(P), last = (P.n + 15) / 16;
   // Waves: eight per tile, fewer where that still gives two rounds of all CUs' sixteen
   const int64_t pieces = (P.k * (I8 ? 1 : 2) + 255) / 256;
   int share = kLayerWaves;
@@ -566,9 +608,10 @@ hipError_t launch_in(const LayerArgs& P, hipStream_t stream) {
 }
 template <bool I8, RowMode MODE>
 hipError_t launch_out(const LayerArgs& P, hipStream_t stream) {
-  const int splits = splits_of(P.k);
-  const dim3 grid(static_cast<unsigned>((P.k + 15) / 16 * splits)), block(kLayerThreads);
-  hipLaunchKernelGGL((layer_out_kernel<I8, MODE>), grid, block, 0, stream, P, splits);
+  const int splits = splits_of(P, I8);
+  const dim3 grid(static_cast<unsigned>(out_tiles(P.k) * splits)), block(kLayerThreads);
+  const size_t sums = sizeof(float) * kLayerWaves * kOutCols * P.tokens;     // at most 64 KB
+  hipLaunchKernelGGL((layer_out_kernel<I8, MODE>), grid, block, sums, stream, P, splits);
   return hipGetLastError();
 }
 // `length`: of a weight row, in elements.
@@ -583,8 +626,8 @@ hipError_t launch_any(const LayerArgs& P, bool in, int64_t length, bool vec, hip
 
 int64_t layer_workspace(const LayerArgs& P) {
   const Space s = space_of(P);
-  const int splits = splits_of(P.k);
-  const int64_t sums = splits > 1 ? 4 * (P.k + 15) / 16 * 16 * P.tokens * splits : 0;
+  const int splits = splits_of(P, false);      // the larger number
+  const int64_t sums = splits > 1 ? 4 * out_tiles(P.k) * kOutCols * P.tokens * splits : 0;
   return reinterpret_cast<char*>(s.sums) - static_cast<char*>(P.workspace) + whole(sums);
 }
 

@@ -279,11 +279,12 @@ int dmuon_row_matmul(const dmuon_row_product_t* d, const void* a, const float* a
 
 size_t dmuon_expert_layer_workspace_size(const dmuon_expert_layer_t* d) {
   if (!d || d->tokens < 1 || d->tokens > kLayerTokens || d->top_k < 1 || d->top_k > kLayerPicks || d->n < 1 ||
-      d->n > kMaxDim || d->k < 1 || d->k > kMaxDim)
+      d->n > kMaxDim || d->k < 1 || d->k > kMaxDim || d->experts < 1)
     return 0;
   LayerArgs P = {};
   P.tokens = static_cast<int32_t>(d->tokens);
   P.top_k = d->top_k;
+  P.experts = d->experts;
   P.n = d->n;
   P.k = d->k;
   return static_cast<size_t>(layer_workspace(P));

@@ -80,7 +80,7 @@ def test_layer_strides_and_guards(lib, int8):
             big[..., :s[name].shape[-1]] = s[name]
             t[name] = big[..., :s[name].shape[-1]]
         out = torch.full((13, k + pad), 5.0, dtype=BF, device=DEV)
-        d = lib.dmuon_expert_layer_t(tokens=11, n=n, k=k, top_k=2)
+        d = lib.dmuon_expert_layer_t(tokens=11, n=n, k=k, experts=6, top_k=2)
         need = lib._lib.dmuon_expert_layer_workspace_size(d)
         ws = torch.full((need + 64,), 7, dtype=torch.uint8, device=DEV)
         side = torch.cuda.Stream()
