@@ -125,7 +125,7 @@ quantize_rows_kernel(RowsArgs P) {
       }
     }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
+    for (int d = 1; d < (T < 64 ? T : 64); d <<= 1) {
       const uint32_t o = __shfl_xor(m, d);
       m = o > m ? o : m;
     }
@@ -139,7 +139,7 @@ quantize_rows_kernel(RowsArgs P) {
     float scale = __uint_as_float(m) * kPerMax;
     if (scale < kScaleMin) scale = kScaleMin;     // a NaN stays
     const float inv = 1.f / scale;
-    if (!in) continue;                      // whole waves with T = 64, never with more
+    if (!in) continue;                      // never with a row per block
     if (t == 0) P.scale[row] = scale;
     int8_t* q = P.q + row * P.cols;
     if constexpr (HELD > 0) {
@@ -208,23 +208,30 @@ dequantize_rows_kernel(RowsArgs P) {
 
 constexpr int64_t kMaxRowBlocks = int64_t(1) << 20;     // blocks go on to further rows
 
-template <bool F32, bool GLU, int T>
+template <bool F32, bool GLU, int T, int HELD>
 void launch_held(const RowsArgs& P, hipStream_t stream) {
   const int64_t blocks = (P.rows + kRowThreads / T - 1) / (kRowThreads / T);
-  const dim3 grid(static_cast<unsigned>(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks)), block(kRowThreads);
-  const int64_t pieces = (P.cols + 8 * T - 1) / (8 * T);
-  if (pieces <= 1) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 1>), grid, block, 0, stream, P);
-  else if (pieces <= 2) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 2>), grid, block, 0, stream, P);
-  else if (pieces <= 4) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 4>), grid, block, 0, stream, P);
-  else if (pieces <= 8) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 8>), grid, block, 0, stream, P);
-  else if constexpr (T > 64) hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, 0>), grid, block, 0, stream, P);
+  const dim3 grid(static_cast<unsigned>(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks));
+  hipLaunchKernelGGL((quantize_rows_kernel<F32, GLU, T, HELD>), grid, dim3(kRowThreads), 0, stream, P);
 }
 
-// A wave per row where a wave holds a row and there are enough of them, else a block.
+// Many rows: sixteen lanes a row of up to 256 columns (65536 x 128: 16.5 us with a
+// wave, 6.9 so), a wave up to 2048 (16384 x 1024: 10.1 us, 15.7 with a block; 8192 x
+// 4096 19.5 and 18.5, gated 32.1 and 28.9).  Few rows or longer ones: a block.
 template <bool F32, bool GLU>
 hipError_t launch_rows(const RowsArgs& P, hipStream_t stream) {
-  if (P.cols <= 64 * 8 * 8 && P.rows >= 1024) launch_held<F32, GLU, 64>(P, stream);
-  else launch_held<F32, GLU, kRowThreads>(P, stream);
+  constexpr int B = kRowThreads;
+  const bool many = P.rows >= 1024;
+  if (many && P.cols <= 128) launch_held<F32, GLU, 16, 1>(P, stream);
+  else if (many && P.cols <= 256) launch_held<F32, GLU, 16, 2>(P, stream);
+  else if (many && P.cols <= 512) launch_held<F32, GLU, 64, 1>(P, stream);
+  else if (many && P.cols <= 1024) launch_held<F32, GLU, 64, 2>(P, stream);
+  else if (many && P.cols <= 2048) launch_held<F32, GLU, 64, 4>(P, stream);
+  else if (P.cols <= 8 * B) launch_held<F32, GLU, B, 1>(P, stream);
+  else if (P.cols <= 16 * B) launch_held<F32, GLU, B, 2>(P, stream);
+  else if (P.cols <= 32 * B) launch_held<F32, GLU, B, 4>(P, stream);
+  else if (P.cols <= 64 * B) launch_held<F32, GLU, B, 8>(P, stream);
+  else launch_held<F32, GLU, B, 0>(P, stream);
   return hipGetLastError();
 }
 
