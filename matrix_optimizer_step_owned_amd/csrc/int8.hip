@@ -546,7 +546,7 @@ template <typename OutT>
 hipError_t launch_matmul(const Int8Args& P, bool vec, hipStream_t stream) {
   const int64_t used = P.offsets ? (P.experts < P.m ? P.experts : P.m) : 1;
   const int64_t big = (P.m / kBig + used) * ((P.n + kBig - 1) / kBig);
-  // offsets of a tile's rows within 31 bits
+  // 256-tiles from 192 on (2048 x 4096 x 4096, 128 of them: 53 us so, 54 in 128-tiles)
   const bool fits = P.lda <= kMaxBigPitch && P.ldb <= kMaxBigPitch && P.experts <= kBigExperts;
   if (vec && fits && big >= 192) {
     const dim3 grid(static_cast<unsigned>(big < kBigBlocks ? big : kBigBlocks)), block(kBigThreads);
@@ -562,8 +562,18 @@ hipError_t launch_matmul(const Int8Args& P, bool vec, hipStream_t stream) {
     }
     if (P.m <= 32 * experts) return launch_skinny<2, 2, OutT>(P, stream);
   }
-  // 64-tiles where 128-tiles would give fewer than one per CU
   auto tiles = [&](int64_t t) { return (P.m / t + used) * ((P.n + t - 1) / t); };
+  // long sums and few tiles (up to 64 and what a last row of them adds): the few-rows
+  // kernel, whose waves split the sum, in the smallest blocks that give about one per
+  // CU (tiles and this: 48 x 1024 x 14336 46.2 and 14.8 us, 256 x 512 x 14336 47.5 and 21.2,
+  // 33 x 4096 x 14336 46.1 and 28.4, 256 x 1024 x 4096 16.3 and 10.0; but 128 x 4096 x 4096 16.0 and 18.3, 1024 x
+  // 256 x 1024 7.2 and 7.6)
+  if (vec && P.k >= 2048 && tiles(64) <= 80) {
+    if (skinny_blocks(P, 1, 1) <= 288) return launch_skinny<1, 1, OutT>(P, stream);
+    if (skinny_blocks(P, 1, 2) <= 288) return launch_skinny<1, 2, OutT>(P, stream);
+    return launch_skinny<2, 2, OutT>(P, stream);
+  }
+  // 64-tiles where 128-tiles would give fewer than one per CU
   const bool small = tiles(128) < 256 && tiles(64) <= kMaxSkinnyBlocks;
   const dim3 grid(static_cast<unsigned>(grouped_grid(tiles(small ? 64 : 128))));
   if (small) launch_tiles<64, OutT>(P, vec, grid, stream);
