@@ -74,12 +74,10 @@ struct RowStep {
 #pragma unroll
     for (int i = 0; i < N; ++i) h[i] = row_chunk<2, MODE>(row, offset(i, at, g), I8 ? 2 * bytes : bytes);
   }
-  // With kWhole the weights' zeros are enough: what is read in their place is the row's own.
+  // The weights' zeros would be enough, but for an Inf of the row, whose product with them is NaN.
   __device__ __forceinline__ void trim(int at, int bytes, int g) {
-    if constexpr (MODE == kMoved) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) trim_chunk<MODE>(h[i], offset(i, at, g), I8 ? 2 * bytes : bytes);
-    }
+    for (int i = 0; i < N; ++i) trim_chunk<MODE>(h[i], offset(i, at, g), I8 ? 2 * bytes : bytes);
   }
 };
 // acc[m] += one step's products with MB blocks of rows; the weights are widened once.
@@ -383,7 +381,10 @@ layer_in_kernel(LayerArgs P, int groups, int tiles, int share) {
         uint16_t* h = space.h + (int64_t(rows.token[i]) * P.top_k + rows.pick[i]) * 2 * part + 16 * int64_t(tile);
         store4<uint16_t>(h, 4 * g, cols, false, y);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) y[q] -= bf16_lo(pack2_bf16(y[q], 0.f));
+        for (int q = 0; q < 4; ++q) {
+          const float rounded = bf16_lo(pack2_bf16(y[q], 0.f));
+          y[q] = __builtin_isinf(rounded) ? 0.f : y[q] - rounded;
+        }
         store4<uint16_t>(h + part, 4 * g, cols, false, y);
       };
       if (share == 1) {

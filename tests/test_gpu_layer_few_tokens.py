@@ -142,6 +142,58 @@ def test_layer_not_finite(lib, int8):
         assert torch.equal(got[~hit], clean[~hit]) and torch.isnan(got[hit]).any(1).all()
 
 
+@pytest.mark.parametrize("int8", [False, True])
+def test_layer_inf_is_not_nan(lib, int8):
+    """An Inf in x with weights of one sign: G x and U x are Inf, and so is y, not NaN, also where
+    the sums end inside the last loads."""
+    for n, k in ((48, 80), (48, 64), (45, 61), (8, 16)):
+        s = make(np.random.default_rng(1), 5, 3, 2, n, k, int8)
+        for name in ("w_in", "w_out"):
+            s[name] = s[name].float().abs().clamp(1, 127).to(s[name].dtype)      # 128 is no int8
+        s["x"] = s["x"].abs()
+        s["x"][2, k - 1] = s["x"][4, 0] = float("inf")
+        got = call(lib, s)
+        assert torch.isfinite(got[[0, 1, 3]]).all()
+        assert (got[[2, 4]] == float("inf")).all()
+
+
+def test_layer_many_tiles(lib):
+    """More tiles than waves: several rounds per block, and one wave, two or all per tile.  The reference
+    and its bound are those of oracle.rows.layer, an expert at a time in float64 on the GPU."""
+    u = 2.0 ** -24
+    for tokens, experts, top_k, n, k, int8 in ((3, 40, 8, 4096, 1040, False), (60, 300, 5, 1030, 272, True),
+                                               (64, 256, 8, 512, 528, False), (64, 4, 2, 2048, 1024, True)):
+        gen = torch.Generator(device=DEV).manual_seed(n)
+        s = make(np.random.default_rng(2), tokens, experts, top_k, 1, 1, int8)
+        s["x"] = torch.randn(tokens, k, generator=gen, device=DEV).to(BF)
+        for name, shape in (("w_in", (experts, 2 * n, k)), ("w_out", (experts, k, n))):
+            w = torch.randn(shape, generator=gen, device=DEV) * 0.05
+            s[name] = (w * 500).round().clamp(-127, 127).to(torch.int8) if int8 else w.to(BF)
+            if int8:
+                s[name[2:] + "_scale"] = torch.rand(shape[:2], generator=gen, device=DEV) / 500
+        got = call(lib, s).double()
+        y, err, mag = (torch.zeros(tokens, k, dtype=torch.float64, device=DEV) for _ in range(3))
+        x = s["x"].double()
+        for e in range(experts):
+            gate = (s["gates"].double() * (s["ids"] == e)).sum(1, keepdim=True)
+            w_in, w_out = s["w_in"][e].double(), s["w_out"][e].double()
+            if int8:
+                w_in, w_out = w_in * s["in_scale"][e].double()[:, None], w_out * s["out_scale"][e].double()[:, None]
+            up, size = x @ w_in.T.contiguous(), (k + 8) * u * (x.abs() @ w_in.abs().T.contiguous())
+            a, b, da, db = up[:, :n], up[:, n:], size[:, :n], size[:, n:]
+            act = torch.nn.functional.silu(a)
+            h = gate * act * b
+            dh = gate.abs() * (1.1 * da * (b.abs() + db) + act.abs() * db) + h.abs() * (2 * a.abs() + 16) * 2 * u
+            dh += 2.0 ** -16 * (h.abs() + dh) + 2.0 ** -133
+            dh *= gate != 0
+            y += h @ w_out.T.contiguous()
+            err += dh @ w_out.abs().T.contiguous()
+            mag += (h.abs() + dh) @ w_out.abs().T.contiguous()
+        err += (2 * n * top_k + 8) * u * mag
+        tol = err + 2.0 ** -8 * (y.abs() + err) + 1e-38
+        assert bool(torch.isfinite(got).all()) and bool(((got - y).abs() <= tol).all()), float(((got - y).abs() / tol).max())
+
+
 def test_layer_graph_two_streams(lib):
     """Two captured calls with workspaces of their own, replayed next to eager ones."""
     rng = np.random.default_rng(4)
