@@ -185,17 +185,21 @@ struct Space {
 };
 __host__ __device__ inline int64_t part_of(int64_t n) { return (n + 7) / 8 * 8; }
 __host__ __device__ inline int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
-__host__ __device__ inline Space space_of(const LayerArgs& P) {
-  Space s;
+struct Offsets {
+  int64_t routing, arrived, sums;      // bytes; h comes first
+};
+__host__ __device__ inline Offsets offsets_of(const LayerArgs& P) {
+  Offsets o;
+  o.routing = whole(int64_t(P.tokens) * P.top_k * 4 * part_of(P.n));
+  o.arrived = o.routing + whole(sizeof(Routing));
+  o.sums = o.arrived + whole((P.k + 15) / 16 * 4);
+  return o;
+}
+__device__ __forceinline__ Space space_of(const LayerArgs& P) {
+  const Offsets o = offsets_of(P);
   char* p = static_cast<char*>(P.workspace);
-  s.h = reinterpret_cast<uint16_t*>(p);
-  p += whole(int64_t(P.tokens) * P.top_k * 4 * part_of(P.n));
-  s.routing = reinterpret_cast<Routing*>(p);
-  p += whole(sizeof(Routing));
-  s.arrived = reinterpret_cast<int32_t*>(p);
-  p += whole((P.k + 15) / 16 * 4);
-  s.sums = reinterpret_cast<float*>(p);
-  return s;
+  return Space{reinterpret_cast<uint16_t*>(p), reinterpret_cast<Routing*>(p + o.routing),
+               reinterpret_cast<int32_t*>(p + o.arrived), reinterpret_cast<float*>(p + o.sums)};
 }
 
 // One block lists the touched experts and their rows.  Which of an expert's rows
@@ -626,10 +630,8 @@ hipError_t launch_any(const LayerArgs& P, bool in, int64_t length, bool vec, hip
 }  // namespace
 
 int64_t layer_workspace(const LayerArgs& P) {
-  const Space s = space_of(P);
   const int splits = splits_of(P, false);      // the larger number
-  const int64_t sums = splits > 1 ? 4 * out_tiles(P.k) * kOutCols * P.tokens * splits : 0;
-  return reinterpret_cast<char*>(s.sums) - static_cast<char*>(P.workspace) + whole(sums);
+  return offsets_of(P).sums + whole(splits > 1 ? 4 * out_tiles(P.k) * kOutCols * P.tokens * splits : 0);
 }
 
 hipError_t launch_layer_in(const LayerArgs& P, bool vec, hipStream_t stream) {
