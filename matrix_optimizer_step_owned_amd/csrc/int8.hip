@@ -474,27 +474,49 @@ int8_matmul_big_kernel(Int8Args P) {
 
 // ---- product, few rows ----------------------------------------------------------
 
+template <RowMode MODE>
 struct Int8Skinny {
   using Acc = i32x4_t;
   const float* sa;      // of the tile's first row
   const float* sb;      // of the tile's first column
+  int k;
 
+  // kMoved: a chunk past the row's end is read where the row ends and put right when it is used.
+  static __device__ __forceinline__ SkinnyFrag load(const char* row, int64_t at, int64_t bytes, int g) {
+    if constexpr (MODE == kWhole) return skinny_load(row, at, bytes, g);
+    SkinnyFrag f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) f.h[h] = row_chunk<1, kMoved>(row, int(at) + 64 * h + 16 * g, int(bytes));
+    return f;
+  }
+  __device__ __forceinline__ SkinnyFrag trimmed(SkinnyFrag f, int at, int g) const {
+    if (MODE == kMoved && at + 128 > k) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) trim_chunk<kMoved>(f.h[h], at + 64 * h + 16 * g, k);
+    }
+    return f;
+  }
   template <int MB, int NB>
-  __device__ __forceinline__ void step(int, int, int, int, const SkinnyFrag (&b)[NB], const SkinnyFrag (&a)[MB],
+  __device__ __forceinline__ void step(int s, int lane, int, int, const SkinnyFrag (&b)[NB], const SkinnyFrag (&a)[MB],
                                        i32x4_t (&acc)[NB][MB]) const {
+    SkinnyFrag x[MB];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int m = 0; m < MB; ++m) x[m] = trimmed(a[m], s * 128, lane >> 4);
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+    for (int n = 0; n < NB; ++n) {
+      const SkinnyFrag w = trimmed(b[n], s * 128, lane >> 4);
 #pragma unroll
-        for (int m = 0; m < MB; ++m) acc[n][m] = multiply(b[n].h[h], a[m].h[h], acc[n][m]);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[n][m] = multiply(w.h[h], x[m].h[h], acc[n][m]);
+    }
   }
   __device__ __forceinline__ f32x4_t finish(const i32x4_t& v, int row, int col, int cols) const {
     return scaled(v, sa[row], four_scales(sb, col, cols));
   }
 };
 
-template <int MB, int NB, int W, typename OutT>
+template <RowMode MODE, int MB, int NB, int W, typename OutT>
 __global__ void __launch_bounds__(64 * W)
 int8_skinny_kernel(Int8Args P) {
   __shared__ __attribute__((aligned(16))) float sums[W * MB * NB * 256];
@@ -508,12 +530,12 @@ int8_skinny_kernel(Int8Args P) {
   }
   if (row0 >= end) return;
   const int64_t j0 = int64_t(tn) * (16 * NB);
-  const Int8Skinny op = {P.a_scale + row0, P.b_scale + e * P.n + j0};
-  skinny_block<Int8Skinny, MB, NB, W, OutT>(op, static_cast<const char*>(P.a) + row0 * P.lda, P.lda,
-                                            static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb, P.ldb,
-                                            static_cast<OutT*>(P.c) + row0 * P.ldc + j0, P.ldc,
-                                            end - row0 < 16 * MB ? end - row0 : 16 * MB,
-                                            int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k, P.accumulate, sums);
+  const Int8Skinny<MODE> op = {P.a_scale + row0, P.b_scale + e * P.n + j0, int(P.k)};
+  skinny_block<Int8Skinny<MODE>, MB, NB, W, OutT>(
+      op, static_cast<const char*>(P.a) + row0 * P.lda, P.lda,
+      static_cast<const char*>(P.b) + e * P.b_stride + j0 * P.ldb, P.ldb, static_cast<OutT*>(P.c) + row0 * P.ldc + j0,
+      P.ldc, end - row0 < 16 * MB ? end - row0 : 16 * MB, int(P.n - j0 < 16 * NB ? P.n - j0 : 16 * NB), P.k,
+      P.accumulate, sums);
 }
 
 int64_t skinny_blocks(const Int8Args& P, int mb, int nb) {
@@ -521,16 +543,20 @@ int64_t skinny_blocks(const Int8Args& P, int mb, int nb) {
   return (P.m / (16 * mb) + used) * ((P.n + 16 * nb - 1) / (16 * nb));
 }
 template <int MB, int NB, typename OutT>
-hipError_t launch_skinny(const Int8Args& P, hipStream_t stream) {
+hipError_t launch_skinny(const Int8Args& P, bool vec, hipStream_t stream) {
   const int64_t blocks = skinny_blocks(P, MB, NB);
   const dim3 grid(static_cast<unsigned>(blocks));
+  if (!vec) {
+    hipLaunchKernelGGL((int8_skinny_kernel<kMoved, MB, NB, 8, OutT>), grid, dim3(512), 0, stream, P);
+    return hipGetLastError();
+  }
   if constexpr (skinny_sixteen(MB, NB, sizeof(OutT) == 4)) {
     if (blocks < kSkinnyWide) {
-      hipLaunchKernelGGL((int8_skinny_kernel<MB, NB, 16, OutT>), grid, dim3(1024), 0, stream, P);
+      hipLaunchKernelGGL((int8_skinny_kernel<kWhole, MB, NB, 16, OutT>), grid, dim3(1024), 0, stream, P);
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((int8_skinny_kernel<MB, NB, 8, OutT>), grid, dim3(512), 0, stream, P);
+  hipLaunchKernelGGL((int8_skinny_kernel<kWhole, MB, NB, 8, OutT>), grid, dim3(512), 0, stream, P);
   return hipGetLastError();
 }
 
@@ -553,14 +579,14 @@ hipError_t launch_matmul(const Int8Args& P, bool vec, hipStream_t stream) {
     hipLaunchKernelGGL((int8_matmul_big_kernel<OutT>), grid, block, 0, stream, P);
     return hipGetLastError();
   }
-  if (vec && skinny_blocks(P, 1, 1) <= kMaxSkinnyBlocks) {
+  if (P.k >= 16 && skinny_blocks(P, 1, 1) <= kMaxSkinnyBlocks) {
     // at most 16, or 32, rows per expert on average
     const int64_t experts = P.offsets ? P.experts : 1;
     if (P.m <= 16 * experts) {
-      if (skinny_blocks(P, 1, 2) >= kSkinnyWide) return launch_skinny<1, 2, OutT>(P, stream);
-      return launch_skinny<1, 1, OutT>(P, stream);
+      if (skinny_blocks(P, 1, 2) >= kSkinnyWide) return launch_skinny<1, 2, OutT>(P, vec, stream);
+      return launch_skinny<1, 1, OutT>(P, vec, stream);
     }
-    if (P.m <= 32 * experts) return launch_skinny<2, 2, OutT>(P, stream);
+    if (P.m <= 32 * experts) return launch_skinny<2, 2, OutT>(P, vec, stream);
   }
   auto tiles = [&](int64_t t) { return (P.m / t + used) * ((P.n + t - 1) / t); };
   // long sums and few tiles (up to 64 and what a last row of them adds): the few-rows
@@ -568,10 +594,10 @@ hipError_t launch_matmul(const Int8Args& P, bool vec, hipStream_t stream) {
   // CU (tiles and this: 48 x 1024 x 14336 46.2 and 14.8 us, 256 x 512 x 14336 47.5 and 21.2,
   // 33 x 4096 x 14336 46.1 and 28.4, 256 x 1024 x 4096 16.3 and 10.0; but 128 x 4096 x 4096 16.0 and 18.3, 1024 x
   // 256 x 1024 7.2 and 7.6)
-  if (vec && P.k >= 2048 && tiles(64) <= 80) {
-    if (skinny_blocks(P, 1, 1) <= 288) return launch_skinny<1, 1, OutT>(P, stream);
-    if (skinny_blocks(P, 1, 2) <= 288) return launch_skinny<1, 2, OutT>(P, stream);
-    return launch_skinny<2, 2, OutT>(P, stream);
+  if (P.k >= 2048 && tiles(64) <= 80) {
+    if (skinny_blocks(P, 1, 1) <= 288) return launch_skinny<1, 1, OutT>(P, vec, stream);
+    if (skinny_blocks(P, 1, 2) <= 288) return launch_skinny<1, 2, OutT>(P, vec, stream);
+    return launch_skinny<2, 2, OutT>(P, vec, stream);
   }
   // 64-tiles where 128-tiles would give fewer than one per CU
   const bool small = tiles(128) < 256 && tiles(64) <= kMaxSkinnyBlocks;

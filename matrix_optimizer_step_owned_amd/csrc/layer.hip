@@ -101,12 +101,14 @@ __device__ __forceinline__ void add_step(const WeightStep<I8, MODE>& w, const Ro
   }
 }
 
-// The ids of a call in LDS, -1 for nobody's.
+// The ids, -1 for nobody's, and the gates of a call in LDS.
 struct Ids {
   int16_t of[kLayerTokens * kLayerPicks];
+  float gate[kLayerTokens * kLayerPicks];
   __device__ __forceinline__ void load(const LayerArgs& P) {
     for (int i = threadIdx.x; i < P.tokens * P.top_k; i += kLayerThreads) {
       const uint32_t id = uint32_t(P.ids[i]);
+      gate[i] = P.gates[i];
       of[i] = id < uint32_t(P.experts) ? int16_t(id) : int16_t(-1);
     }
   }
@@ -155,7 +157,7 @@ struct ExpertRows {
     if (first >= 0) {
       float g = 0.f;
       for (int j = first; j < P.top_k; ++j)
-        if (ids.of[lane * P.top_k + j] == e) g += P.gates[lane * P.top_k + j];
+        if (ids.of[lane * P.top_k + j] == e) g += ids.gate[lane * P.top_k + j];
       const int i = __popcll(rows & ((uint64_t(1) << lane) - 1));
       token[i] = lane;
       pick[i] = first;
@@ -265,14 +267,15 @@ __device__ __forceinline__ void list_rows(const LayerArgs& P, const Ids& ids, Ro
 template <bool I8, RowMode MODE, int MB>
 __global__ void __launch_bounds__(kLayerThreads, MB == 1 ? 4 : 2)
 layer_in_kernel(LayerArgs P, int groups, int tiles, int share) {
-  constexpr int U = 2, W = kLayerWaves;
+  constexpr int U = I8 && MB == 4 ? 1 : 2, W = kLayerWaves;
   __shared__ Ids ids;
   union Scratch {
     ExpertRows rows;
     RoutingScratch list;
   };
   __shared__ Scratch shared;
-  __shared__ __attribute__((aligned(16))) float sums[2][W * 2 * MB * 256];
+  constexpr int BUFS = MB == 4 ? 1 : 2;      // two spare a barrier
+  __shared__ __attribute__((aligned(16))) float sums[BUFS][W * 2 * MB * 256];
   const int slot = int(blockIdx.x) / groups, group = int(blockIdx.x) - slot * groups;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Space space = space_of(P);
@@ -401,7 +404,8 @@ layer_in_kernel(LayerArgs P, int groups, int tiles, int share) {
 #pragma unroll
           for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       } else {
-        float* buf = sums[turn & 1];
+        if (BUFS == 1 && turn > 0) plain_barrier();      // the sums of the round before are read
+        float* buf = sums[turn & (BUFS - 1)];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -432,15 +436,15 @@ layer_in_kernel(LayerArgs P, int groups, int tiles, int share) {
 
 // kOutCols columns of y for all tokens, or one of `splits` parts of their sums.  The
 // sums run over units: U steps of an expert's rows.  Every wave has a run of
-// them and keeps 16 rows' sums in registers while the expert stays the same.  A
+// them and keeps 16 MB rows' sums in registers while the expert stays the same.  A
 // load of h, with its two parts and rows that 16 lanes share, takes the load path as long as one of
 // weights, so each serves two blocks of 16 columns (one token, two experts of
 // 14336 x 4096: 54.7 us with one block, 47.0 with two, 46.5 with four; the 32 tokens in 8 bits
 // 62.5, 48.4, 57.4).
 constexpr int kOutBlocks = 2, kOutCols = 16 * kOutBlocks;
 constexpr int kMaxSplits = 16;
-template <bool I8, RowMode MODE>
-__global__ void __launch_bounds__(kLayerThreads, 4)
+template <bool I8, RowMode MODE, int MB>
+__global__ void __launch_bounds__(kLayerThreads, MB == 1 ? 4 : 2)
 layer_out_kernel(LayerArgs P, int splits) {
   constexpr int U = I8 ? 1 : 2, W = kLayerWaves, NB = kOutBlocks;
   __shared__ uint16_t experts[kLayerExperts], first[kLayerExperts + 1];
@@ -488,50 +492,69 @@ layer_out_kernel(LayerArgs P, int splits) {
       scale[b] = f32x4_t{1.f, 1.f, 1.f, 1.f};
       if constexpr (I8) scale[b] = four_scales(P.out_scale + e * P.k + c0, 16 * b + 4 * g, cols);
     }
-    for (int r0 = lo; r0 < hi; r0 += 16) {
+    for (int r0 = lo; r0 < hi; r0 += 16 * MB) {
       // rows past the last one read it again: their sums are not used
-      const bool has = r0 + r < hi;
-      const int row = list[has ? r0 + r : hi - 1], t = row >> 6;
-      const char* hp = reinterpret_cast<const char*>(space.h + (int64_t(t) * P.top_k + (row & 63)) * 2 * part);
-      f32x4_t acc[NB][1];
+      const char* hp[MB];
+      int token[MB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[b][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int m = 0; m < MB; ++m) {
+        const int i = r0 + 16 * m + r, row = list[i < hi ? i : hi - 1];
+        token[m] = i < hi ? row >> 6 : -1;
+        hp[m] = reinterpret_cast<const char*>(space.h + (int64_t(row >> 6) * P.top_k + (row & 63)) * 2 * part);
+      }
+      f32x4_t acc[NB][MB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       for (int s0 = unit * U; s0 < (unit + n) * U; s0 += U) {
         WeightStep<I8, MODE> w[U][NB];
-        RowStep<I8, MODE> x[U][2][1];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int b = 0; b < NB; ++b) w[u][b].load(weights[b] + expert, (s0 + u) * 128, bytes, g);
+        // one part of h at a time where there are many rows: their registers are the bound
+        constexpr int Q = MB == 4 ? 1 : 2;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int q0 = 0; q0 < 2; q0 += Q) {
+          RowStep<I8, MODE> x[U][Q][MB];
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            x[u][q][0].load(hp + q * part * 2, (s0 + u) * 128, bytes, g);
-        if ((s0 + U) * 128 > bytes) {
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
+            for (int q = 0; q < Q; ++q)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) w[u][b].trim((s0 + u) * 128, bytes, g);
+              for (int m = 0; m < MB; ++m) x[u][q][m].load(hp[m] + (q0 + q) * part * 2, (s0 + u) * 128, bytes, g);
+          if ((s0 + U) * 128 > bytes) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) x[u][q][0].trim((s0 + u) * 128, bytes, g);
+            for (int u = 0; u < U; ++u) {
+              if (q0 == 0) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) w[u][b].trim((s0 + u) * 128, bytes, g);
+              }
+#pragma unroll
+              for (int q = 0; q < Q; ++q)
+#pragma unroll
+                for (int m = 0; m < MB; ++m) x[u][q][m].trim((s0 + u) * 128, bytes, g);
+            }
           }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+              for (int q = 0; q < Q; ++q) add_step<I8, MODE, MB>(w[u][b], x[u][q], acc[b]);
+              if constexpr (I8) __builtin_amdgcn_sched_barrier(0);    // one widened step at a time
+            }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) add_step<I8, MODE, 1>(w[u][b], x[u][q], acc[b]);
-            if constexpr (I8) __builtin_amdgcn_sched_barrier(0);    // one widened step at a time
-          }
       }
       // only the expert's own tokens: a weight that is not finite is nobody else's
-      if (has) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        if (token[m] < 0) continue;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          f32x4_t* sum = reinterpret_cast<f32x4_t*>(&sums[wave * width + t * kOutCols + 16 * b + 4 * g]);
-          *sum += acc[b][0] * scale[b];
+          f32x4_t* sum = reinterpret_cast<f32x4_t*>(&sums[wave * width + token[m] * kOutCols + 16 * b + 4 * g]);
+          *sum += acc[b][m] * scale[b];
         }
       }
     }
@@ -591,6 +614,15 @@ int splits_of(const LayerArgs& P, bool i8) {
   return int(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
 
+// Blocks of 16 rows that share one load of the weights: as many as hold twice an
+// expert's rows on average, or all tokens; an expert with more reads its weights again (44 tokens,
+// 6 of 8 experts of 9472 x 1920: ONE us with one, TWO with two, FOUR with four).
+int row_blocks(const LayerArgs& P) {
+  const int64_t picks = int64_t(P.tokens) * P.top_k;
+  if (P.tokens <= 16 || picks <= 8 * int64_t(P.experts)) return 1;
+  return P.tokens <= 32 || picks <= 16 * int64_t(P.experts) ? 2 : 4;
+}
+
 template <bool I8, RowMode MODE>
 hipError_t launch_in(const LayerArgs& P, hipStream_t stream) {
   const int64_t picks = int64_t(P.tokens) * P.top_k, slots = slots_of(P), last = (P.n + 15) / 16;
@@ -604,11 +636,11 @@ hipError_t launch_in(const LayerArgs& P, hipStream_t stream) {
   rounds = rounds < 1 ? 1 : rounds > 8 ? 8 : rounds;
   const int64_t tiles = rounds * once, groups = (last + tiles - 1) / tiles;
   const dim3 grid(static_cast<unsigned>(slots * groups + 1)), block(kLayerThreads);
-  // two blocks of 16 rows where experts are likely to have more than 16
-  if (P.tokens > 16 && picks > 8 * int64_t(P.experts))
-    hipLaunchKernelGGL((layer_in_kernel<I8, MODE, 2>), grid, block, 0, stream, P, int(groups), int(tiles), share);
-  else
-    hipLaunchKernelGGL((layer_in_kernel<I8, MODE, 1>), grid, block, 0, stream, P, int(groups), int(tiles), share);
+  switch (row_blocks(P)) {
+    case 4: hipLaunchKernelGGL((layer_in_kernel<I8, MODE, 4>), grid, block, 0, stream, P, int(groups), int(tiles), share); break;
+    case 2: hipLaunchKernelGGL((layer_in_kernel<I8, MODE, 2>), grid, block, 0, stream, P, int(groups), int(tiles), share); break;
+    default: hipLaunchKernelGGL((layer_in_kernel<I8, MODE, 1>), grid, block, 0, stream, P, int(groups), int(tiles), share);
+  }
   return hipGetLastError();
 }
 template <bool I8, RowMode MODE>
@@ -616,7 +648,11 @@ hipError_t launch_out(const LayerArgs& P, hipStream_t stream) {
   const int splits = splits_of(P, I8);
   const dim3 grid(static_cast<unsigned>(out_tiles(P.k) * splits)), block(kLayerThreads);
   const size_t sums = sizeof(float) * kLayerWaves * kOutCols * P.tokens;     // at most 64 KB
-  hipLaunchKernelGGL((layer_out_kernel<I8, MODE>), grid, block, sums, stream, P, splits);
+  switch (row_blocks(P)) {
+    case 4: hipLaunchKernelGGL((layer_out_kernel<I8, MODE, 4>), grid, block, sums, stream, P, splits); break;
+    case 2: hipLaunchKernelGGL((layer_out_kernel<I8, MODE, 2>), grid, block, sums, stream, P, splits); break;
+    default: hipLaunchKernelGGL((layer_out_kernel<I8, MODE, 1>), grid, block, sums, stream, P, splits);
+  }
   return hipGetLastError();
 }
 // `length`: of a weight row, in elements.

@@ -20,22 +20,27 @@ struct SkinnyFrag {
   u32x4_t h[2];
 };
 
-// 32 bytes of the 128 from p on: those at 16 g and at 64 + 16 g; bytes past
-// `left` read as zero.
-__device__ __forceinline__ SkinnyFrag skinny_load(const char* p, int g, int left) {
+// 32 bytes of the 128 from byte `at` of a row of `bytes` bytes on: those at 16 g and
+// at 64 + 16 g; bytes past the row read as zero.
+__device__ __forceinline__ SkinnyFrag skinny_load(const char* row, int64_t at, int64_t bytes, int g) {
   SkinnyFrag f;
   f.h[0] = u32x4_t{0, 0, 0, 0};
   f.h[1] = u32x4_t{0, 0, 0, 0};
-  if (16 * g < left) f.h[0] = *reinterpret_cast<const u32x4_t*>(p + 16 * g);
-  if (64 + 16 * g < left) f.h[1] = *reinterpret_cast<const u32x4_t*>(p + 64 + 16 * g);
+  const int64_t rest = bytes - at;
+  const int left = rest < 0 ? 0 : rest > 128 ? 128 : int(rest);
+  if (16 * g < left) f.h[0] = *reinterpret_cast<const u32x4_t*>(row + at + 16 * g);
+  if (64 + 16 * g < left) f.h[1] = *reinterpret_cast<const u32x4_t*>(row + at + 64 + 16 * g);
   return f;
 }
 
-// Op: Acc, the accumulators' type (four floats or ints); step(...) adds one step's
-// products; finish(sums, row, first column, columns) turns a lane's four sums into
-// results.
+// Op: Acc, the accumulators' type (four floats or ints); load(row, byte, row's bytes, g) a
+// fragment; step(...) adds one step's products; finish(sums, row, first column,
+// columns) turns a lane's four sums into results.
 struct SkinnyFloat {
   using Acc = f32x4_t;
+  static __device__ __forceinline__ SkinnyFrag load(const char* row, int64_t at, int64_t bytes, int g) {
+    return skinny_load(row, at, bytes, g);
+  }
   __device__ __forceinline__ f32x4_t finish(const f32x4_t& v, int, int, int) const { return v; }
 };
 template <class Op, int MB, int NB, int W, typename OutT>
@@ -70,12 +75,10 @@ __device__ __forceinline__ void skinny_block(const Op& op, const char* a, int64_
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t at = int64_t(s0 + u) * 128;
-      const int64_t rest = row_bytes - at;
-      const int left = rest < 0 ? 0 : rest > 128 ? 128 : int(rest);
 #pragma unroll
-      for (int n = 0; n < NB; ++n) fb[u][n] = skinny_load(bp[n] + at, g, left);
+      for (int n = 0; n < NB; ++n) fb[u][n] = Op::load(bp[n], at, row_bytes, g);
 #pragma unroll
-      for (int m = 0; m < MB; ++m) fa[u][m] = skinny_load(ap[m] + at, g, left);
+      for (int m = 0; m < MB; ++m) fa[u][m] = Op::load(ap[m], at, row_bytes, g);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
