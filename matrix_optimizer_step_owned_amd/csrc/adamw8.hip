@@ -155,7 +155,7 @@ __device__ __forceinline__ u32x2_t to_nearest(const float (&x)[8], float inv) {
   return w;
 }
 
-// A 32-bit hash: the finaliser of MurmurHash3 (A. Appleby, public domain) of x + 0x9e3779b9.
+// A 32-bit hash: the finaliser of MurmurHash3 (by A. Appleby, in the public domain) of x + 0x9e3779b9.
 __host__ __device__ inline uint32_t mix(uint32_t x) {
   x += 0x9e3779b9u;
   x = (x ^ (x >> 16)) * 0x85ebca6bu;

@@ -614,12 +614,14 @@ int splits_of(const LayerArgs& P, bool i8) {
   return int(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
 
-// Blocks of 16 rows that share one load of the weights: as many as hold twice an
-// expert's rows on average, or all tokens; an expert with more reads its weights again (44 tokens,
-// 6 of 8 experts of 9472 x 1920: ONE us with one, TWO with two, FOUR with four).
+// Blocks of 16 rows that share one load of the weights, by an expert's rows on average:
+// two from four rows on, four from 16 on where there are more than 32 tokens; an expert with more
+// rows than that reads its weights again (one, two and four blocks: 44 tokens, 6 of 8 experts of
+// 9472 x 1920 490, 427 and 360 us; 64 tokens, 2 of 8 of 14336 x 4096 972, 730, 774; 64 tokens, 8 of 128
+// of 1024 x 2048 361, 331, 372; 4 tokens, 2 of 8 of 14336 x 4096 299, 327, 394).
 int row_blocks(const LayerArgs& P) {
   const int64_t picks = int64_t(P.tokens) * P.top_k;
-  if (P.tokens <= 16 || picks <= 8 * int64_t(P.experts)) return 1;
+  if (P.tokens <= 16 || picks < 4 * int64_t(P.experts)) return 1;
   return P.tokens <= 32 || picks <= 16 * int64_t(P.experts) ? 2 : 4;
 }
 
