@@ -332,9 +332,11 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], stream=No
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        ts = _torch_stream(stream, device)
-        with torch.cuda.stream(ts):
+        if stream is None:      # the device's current stream owns what is allocated
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(_torch_stream(stream, device)):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace needs {nbytes} bytes")
     return workspace, workspace.numel() * workspace.element_size()
@@ -860,8 +862,11 @@ def _no_graph(name: str, *tensors) -> None:
 def _result(device, stream, shape, dtype, zero=False) -> torch.Tensor:
     """A result allocated here: it belongs to the stream the call runs on (see
     _workspace)."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
     with torch.cuda.stream(_torch_stream(stream, device)):
-        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
 
 
 def _rows2(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
