@@ -940,7 +940,7 @@ def dmuon_expert_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     (x tokens x k, w experts x n x k, offsets int32 on the device).  Rows of no
     expert are left as they were in ``out``, and are zero in an allocated result.
 
-    This call and the five below record no autograd graph and refuse tensors
+    This call and those below record no autograd graph and refuse tensors
     that require a gradient where one would be recorded: call them under
     torch.no_grad(), or in a torch.autograd.Function whose backward calls
     dmuon_expert_input_grad and dmuon_expert_weight_grad."""

@@ -16,7 +16,7 @@
 // touched is device data: layer_in has blocks for as many experts as there can
 // be and each finds its own from the ids.  One block more lists the touched
 // experts and their rows for layer_out, where every wave runs over a part of
-// (expert, steps of its rows) for 16 output columns and adds the rows' sums to
+// (expert, steps of its rows) for 32 output columns and adds the rows' sums to
 // the tokens' in LDS; waves, and blocks that split the same columns, add up
 // in a fixed order, so results do not depend on the order of execution.
 #include "bigtile.h"
@@ -263,7 +263,8 @@ __device__ __forceinline__ void list_rows(const LayerArgs& P, const Ids& ids, Ro
 // block.  `share` waves split the sum of a tile: one where there are tiles for all
 // waves, which then neither wait nor add up (32 tokens, 8 of 128 experts of 1024 x
 // 2048 in 8 bits: 137 us with eight, 87 with one); otherwise they add up in LDS in
-// wave order, one wave for all, another for each round, while the others go on.
+// wave order, one wave for all, another for each round, while the others go on.  One
+// token, two experts of 14336 x 4096 in bf16: 82 us, 5.7 TB/s of weights; the 32 tokens 5.4.
 template <bool I8, RowMode MODE, int MB>
 __global__ void __launch_bounds__(kLayerThreads, MB == 1 ? 4 : 2)
 layer_in_kernel(LayerArgs P, int groups, int tiles, int share) {

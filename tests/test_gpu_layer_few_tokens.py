@@ -219,6 +219,24 @@ def test_layer_graph_two_streams(lib):
         assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(want, outs, again))
 
 
+def test_layer_repeats_bit_for_bit(lib):
+    """Blocks that split the same columns join in a fixed order: many calls in a row, inputs in turn in one
+    workspace, with copies on another stream beside them."""
+    side, big = torch.cuda.Stream(), torch.zeros(1 << 26, device=DEV)
+    copy = torch.empty_like(big)
+    for args in ((5, 16, 3, 515, 1000, False), (20, 32, 4, 256, 512, True), (40, 8, 2, 512, 256, False)):
+        ss = [make(np.random.default_rng(i), *args) for i in range(2)]
+        want = [call(lib, s) for s in ss]
+        ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+        wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+        for i in range(200):
+            if i % 20 == 0:
+                with torch.cuda.stream(side):
+                    copy.copy_(big)
+            wrong += (call(lib, ss[i % 2], workspace=ws) != want[i % 2]).sum()
+        assert int(wrong) == 0
+
+
 def test_layer_far_weights(lib):
     """Experts more than 2^32 bytes apart."""
     rng = np.random.default_rng(5)
