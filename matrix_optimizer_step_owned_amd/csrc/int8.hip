@@ -466,9 +466,10 @@ struct Int8Big {
   }
 };
 
-// 8192 x 14336 x 4096: 354 us, 2.72 POP/s, the board at its power cap (the same loop in
-// bf16 1.4 PFLOP/s; the library's own 8-bit product of 8192^3 2.10, this one 2.74).  A
-// tile's scales and stores cost 1 to 3 us of 69 in 8192 x 4096 x 2048.
+// 8192 x 14336 x 4096: 354 us, 2.72 POP/s; without a break for four seconds 373 us, 2.58
+// (8192^3: 2.74, the library's own 8-bit product 2.10).  A stage takes as long as one of
+// as many bytes in bf16; a tile's scales and stores cost 1 to 3 us of 69 in 8192 x 4096 x
+// 2048, so the loop itself is what bounds it.
 template <typename OutT>
 __global__ void __launch_bounds__(kBigThreads)
 int8_matmul_big_kernel(Int8Args P) {
