@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import itertools
 import json
+import math
 import operator
 import os
 import struct
@@ -1119,9 +1120,11 @@ def dmuon_quantize_rows(x: torch.Tensor, *, activation: Optional[str] = None, q:
     if x.dim() > 2:
         if not x.is_contiguous():
             raise ValueError("x of more than two dimensions must be contiguous")
-        rows, ldx = x.numel() // max(wide, 1), wide
+        rows, ldx = math.prod(lead), wide
     else:
         rows, _, ldx = _rows2(x, "x")
+    if rows and not wide:
+        raise ValueError("rows must have columns")
     if act and wide % 2:
         raise ValueError("gate and up must have the same number of columns")
     cols = wide // 2 if act else wide

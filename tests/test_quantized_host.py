@@ -184,6 +184,10 @@ def test_binding_refusals(dm):
             dm.dmuon_quantize_rows(bad)
     with pytest.raises(ValueError):
         dm.dmuon_quantize_rows(x[:, :5], activation="swiglu")
+    for none in (x[:, :0], x.view(2, 2, 6)[..., :0].contiguous()):
+        for act in (None, "swiglu"):
+            with pytest.raises(ValueError, match="columns"):
+                dm.dmuon_quantize_rows(none, activation=act)
     with pytest.raises(KeyError):
         dm.dmuon_quantize_rows(x, activation="gelu")
     with pytest.raises(ValueError):
