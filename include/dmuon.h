@@ -548,7 +548,8 @@ int dmuon_block_matmul(const dmuon_block_product_t* d, const void* a, const floa
  * the 32-bit finaliser of MurmurHash3 of its argument + 0x9e3779b9 (all modulo
  * 2^32).  The same call on the same state gives the same bits; another step or
  * seed other random numbers.  Every fp32 operation up to r is rounded by itself.
- * A NaN or Inf in a gradient makes the states of its block of 128 NaN;
+ * A NaN or Inf in a gradient makes both scales of its block of 128 not finite (one
+ * whose square overflows fp32 that of the roots), and what they scale NaN or Inf;
  * parameters of its neighbours follow from the next step on.
  * Tensors without a gradient (NULL) or elements are left as they are.  Any
  * numel 0..2^42, buffers aligned to their elements.  No workspace: the tables

@@ -237,6 +237,23 @@ def test_layer_repeats_bit_for_bit(lib):
         assert int(wrong) == 0
 
 
+def test_profile_report(lib):
+    """The kernels' names and launches in a profile."""
+    s = make(np.random.default_rng(3), 5, 16, 3, 515, 1000, True)
+    call(lib, s)
+    x = torch.randn(40, 512, device=DEV)
+    p, st = x.clone(), lib.dmuon_adamw_quantized_state(x)
+    lib.dmuon_profile_begin()
+    call(lib, s)
+    q, sc = lib.dmuon_quantize_rows(x)
+    lib.dmuon_dequantize_rows(q, sc)
+    lib.dmuon_row_matmul(q, sc, q, sc)
+    lib.dmuon_adamw_step_quantized([p], [x], [st[0]], [st[1]], [st[2]], [st[3]], step=1)
+    got = lib.dmuon_profile_end()["kernels"]
+    for name in ("layer_in", "layer_out", "quantize_rows", "dequantize_rows", "int8_matmul", "adamw8"):
+        assert got[name]["launches"] == 1, name
+
+
 def test_layer_far_weights(lib):
     """Experts more than 2^32 bytes apart."""
     rng = np.random.default_rng(5)
