@@ -185,7 +185,7 @@ __device__ __forceinline__ const Adam8Table& table() {
 // One block per 8192 elements of a tensor; a thread holds eight consecutive
 // elements at a time, sixteen lanes a block of 128, whose maximum is four
 // rotations within their row of the wave.  Bound by HBM: 128256 x 2048 and 57 vectors
-// in bf16 511 us, 5.2 TB/s of mixed reads and writes (a copy: 4.8), 10.1 bytes per
+// in bf16 511 to 528 us, 5.0 to 5.2 TB/s of mixed reads and writes (a copy: 4.8), 10.1 bytes per
 // element; nothing is read or written twice.
 __global__ void __launch_bounds__(kAdam8Threads)
 adamw8_kernel(Adam8Table) {

@@ -466,7 +466,7 @@ struct Int8Big {
   }
 };
 
-// 8192 x 14336 x 4096: 354 us, 2.72 POP/s; without a break for four seconds 373 us, 2.58
+// 8192 x 14336 x 4096: 354 to 367 us, 2.62 to 2.72 POP/s; without a break for four seconds 373 us, 2.58
 // (8192^3: 2.74, the library's own 8-bit product 2.10).  A stage takes as long as one of
 // as many bytes in bf16; a tile's scales and stores cost 1 to 3 us of 69 in 8192 x 4096 x
 // 2048, so the loop itself is what bounds it.
